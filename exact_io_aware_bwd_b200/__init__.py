@@ -12,5 +12,7 @@ from .binding import (  # noqa: F401
     fa_bwd_dropout, fa_bwd_window, fa_bwd_workspace_bytes, fa_fwd, fa_fwd_dropout,
     fa_fwd_window, fa_get_device_status, fa_peek_device_status_word,
     fa_selftest_wait_timeout, fa_set_bwd_max_blocks, fa_set_profile_events, fa_status_string, fa_bwd_noalloc, load,
+    attention_decode_prefix, attention_fwd_paged, cache_append, fa_append_paged, fa_decode_prefix,
+    fa_decode_prefix_workspace_bytes, fa_fwd_paged, fa_fwd_paged_workspace_bytes,
     KERNEL_FWD, KERNEL_BWD_MAIN,
 )

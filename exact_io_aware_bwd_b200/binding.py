@@ -75,6 +75,17 @@ def load():
             lib.fa_decode_workspace_bytes.restype = ctypes.c_size_t
             lib.fa_decode_paged.argtypes = ([vp] * 7 + [i] * 8 + [f, i, vp, ctypes.c_size_t, vp])
             lib.fa_decode_paged.restype = i
+            i64p, sz = ctypes.POINTER(ctypes.c_int64), ctypes.c_size_t
+            lib.fa_append_paged.argtypes = [vp, vp, vp, i64p] + [vp] * 8 + [i] * 10 + [i, vp]
+            lib.fa_append_paged.restype = i
+            lib.fa_fwd_paged_workspace_bytes.argtypes = [i] * 7
+            lib.fa_fwd_paged_workspace_bytes.restype = sz
+            lib.fa_fwd_paged.argtypes = [vp] * 8 + [i] * 8 + [f, i, vp, sz, vp]
+            lib.fa_fwd_paged.restype = i
+            lib.fa_decode_prefix_workspace_bytes.argtypes = [i] * 8
+            lib.fa_decode_prefix_workspace_bytes.restype = sz
+            lib.fa_decode_prefix.argtypes = [vp] * 7 + [i] * 9 + [f, i, vp, sz, vp]
+            lib.fa_decode_prefix.restype = i
             lib.fa_get_device_status.argtypes = [vp]
             lib.fa_get_device_status.restype = i
             lib.fa_peek_device_status_word.argtypes = [vp]
@@ -368,7 +379,197 @@ def fa_decode_paged(q, k_cache, v_cache, block_table, seq_lens, o, lse, scale: f
     _check(st, "fa_decode_paged")
 
 
+# ------------------------------------------------------------ paged cache
+
+def _on_device(t, stream):
+    """(context that makes t's device current, stream argument): the default
+    stream is the current one of the tensors' device, whichever device is
+    current when the call is made."""
+    return torch.cuda.device(t.device), torch.cuda.current_stream(t.device) if stream is None else stream
+
+
+def _paged_dims(where, q, k_cache, v_cache, block_table, seq_lens, new_lens=None, heads=None):
+    """Checks of the cache (`heads` kv heads when given), its table and
+    lengths; returns (B, Hq, N, d, P, Hkv, num_pages, max_pages)."""
+    for name, t, dim in (("q", q, 4), ("k_cache", k_cache, 4), ("v_cache", v_cache, 4), ("block_table", block_table, 2),
+                         ("seq_lens", seq_lens, 1)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{where}: {name} must be a tensor")
+        if t.dim() != dim:
+            raise ValueError(f"{where}: {name} must be {dim}-D, got {tuple(t.shape)}")
+    B, Hq, N, d = q.shape
+    num_pages, Hkv, P, _ = k_cache.shape
+    if q.dtype not in _DTYPES:
+        raise TypeError(f"{where}: q has dtype {q.dtype}, expected bfloat16 or float16")
+    if heads is not None and Hkv != heads:
+        raise ValueError(f"{where}: k has {heads} heads, the cache {Hkv}")
+    same, cache, i32 = (q.dtype,), (num_pages, Hkv, P, d), (torch.int32,)
+    _expect(where, ("k_cache", k_cache, cache, same), ("v_cache", v_cache, cache, same),
+            ("block_table", block_table, (B, block_table.shape[1]), i32), ("seq_lens", seq_lens, (B,), i32),
+            ("new_lens", new_lens, (B,), i32))
+    if q.device != k_cache.device:
+        raise ValueError(f"{where}: all tensors must be on one device (q is on {q.device})")
+    return B, Hq, N, d, P, Hkv, num_pages, block_table.shape[1]
+
+
+def _row_strides(where, name, t, shape, dtype):
+    """(batch, head, token) strides of a [B, H, N, d] tensor whose rows are
+    contiguous; a dimension of one entry or none is never stepped over."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{where}: {name} has dtype {t.dtype}, expected {dtype}")
+    if t.stride(3) != 1:
+        raise ValueError(f"{where}: the rows of {name} must be contiguous")
+    return [t.stride(i) if t.shape[i] > 1 else 0 for i in range(3)]
+
+
+def fa_append_paged(q, k, v, q_out, k_out, k_cache, v_cache, block_table, seq_lens, new_lens, inv_freq,
+                    interleaved: bool = False, stream=None) -> None:
+    """Appends k, v [B,Hkv,N,d] to a paged cache [pages,Hkv,P,d], k rotated by
+    its position; q [B,Hq,N,d] is rotated into q_out (both None: keys and
+    values only), and the rotated k also written to k_out when given.  q, k, v
+    may be strided (contiguous rows); seq_lens [B] counts the new tokens, of
+    which sequence b has new_lens[b] (None: N); inv_freq fp32 [rot/2] or None
+    (no rotation)."""
+    where = "fa_append_paged"
+    if (q is None) != (q_out is None):
+        raise ValueError(f"{where}: q and q_out come together")
+    for name, t in (("k", k), ("v", v)) + ((("q", q),) if q is not None else ()):
+        if not isinstance(t, torch.Tensor) or t.dim() != 4:
+            raise ValueError(f"{where}: {name} must be 4-D [B, H, N, d]")
+    if k.dtype not in _DTYPES:
+        raise TypeError(f"{where}: k has dtype {k.dtype}, expected bfloat16 or float16")
+    B, Hkv, N, d = k.shape
+    Hq = Hkv if q is None else q.shape[1]
+    strides = [0, 0, 0] if q is None else _row_strides(where, "q", q, (B, Hq, N, d), k.dtype)
+    strides = strides + _row_strides(where, "k", k, (B, Hkv, N, d), k.dtype) \
+        + _row_strides(where, "v", v, (B, Hkv, N, d), k.dtype)
+    if inv_freq is not None and (not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1):
+        raise ValueError(f"{where}: inv_freq must be a 1-D tensor")
+    rot = 0 if inv_freq is None else 2 * inv_freq.shape[0]
+    _, _, _, _, P, _, num_pages, max_pages = _paged_dims(where, k, k_cache, v_cache, block_table, seq_lens, new_lens,
+                                                          heads=Hkv)
+    _expect(where, ("k_cache", k_cache, None, None), ("q_out", q_out, (B, Hq, N, d), (k.dtype,)),
+            ("k_out", k_out, (B, Hkv, N, d), (k.dtype,)), ("inv_freq", inv_freq, None, (torch.float32,)))
+    for name, t in (("q", q), ("v", v)):
+        if t is not None and t.device != k.device:
+            raise ValueError(f"{where}: all tensors must be on one device ({name} is on {t.device})")
+    device, stream = _on_device(k, stream)
+    with device:
+        st = load().fa_append_paged(_ptr(q), _ptr(k), _ptr(v), (ctypes.c_int64 * 9)(*strides), _ptr(q_out),
+                                    _ptr(k_out), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(seq_lens),
+                                    _ptr(new_lens), _ptr(inv_freq), B, Hq, Hkv, N, d, P, max_pages, num_pages, rot,
+                                    int(bool(interleaved)), _DTYPES[k.dtype], _stream(stream))
+    _check(st, where)
+
+
+def fa_fwd_paged_workspace_bytes(B: int, Hq: int, Hkv: int, N: int, d: int, page_size: int, max_pages: int) -> int:
+    return int(load().fa_fwd_paged_workspace_bytes(B, Hq, Hkv, N, d, page_size, max_pages))
+
+
+def fa_fwd_paged(q, k_cache, v_cache, block_table, seq_lens, new_lens, o, lse, scale: float, workspace,
+                 stream=None) -> None:
+    """Forward pass of new tokens over a paged cache that already holds them:
+    q [B,Hq,N,d], token t < new_lens[b] (None: N) at position
+    seq_lens[b] - new_lens[b] + t sees every key up to its own; workspace of
+    at least fa_fwd_paged_workspace_bytes(...) bytes."""
+    where = "fa_fwd_paged"
+    B, Hq, N, d, P, Hkv, num_pages, max_pages = _paged_dims(where, q, k_cache, v_cache, block_table, seq_lens, new_lens)
+    _expect(where, ("q", q, None, None), ("o", o, (B, Hq, N, d), (q.dtype,)), ("lse", lse, (B, Hq, N), (torch.float32,)),
+            ("workspace", workspace, None, None))
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    device, stream = _on_device(q, stream)
+    with device:
+        st = load().fa_fwd_paged(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(seq_lens), _ptr(new_lens),
+                                 _ptr(o), _ptr(lse), B, Hq, Hkv, N, d, P, max_pages, num_pages, float(scale),
+                                 _DTYPES[q.dtype], _ptr(workspace), ws_bytes, _stream(stream))
+    _check(st, where)
+
+
+def fa_decode_prefix_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, d: int, page_size: int, max_pages: int,
+                                     prefix_len: int) -> int:
+    return int(load().fa_decode_prefix_workspace_bytes(B, Hq, Hkv, Nq, d, page_size, max_pages, prefix_len))
+
+
+def fa_decode_prefix(q, k_cache, v_cache, block_table, seq_lens, o, lse, scale: float, prefix_len: int, workspace,
+                     stream=None) -> None:
+    """fa_decode_paged for a batch whose first prefix_len tokens (a multiple of
+    the page size) are the same pages in every sequence: they are read once,
+    from the pages of sequence 0.  workspace of at least
+    fa_decode_prefix_workspace_bytes(...) bytes."""
+    where = "fa_decode_prefix"
+    B, Hq, N, d, P, Hkv, num_pages, max_pages = _paged_dims(where, q, k_cache, v_cache, block_table, seq_lens)
+    _expect(where, ("q", q, None, None), ("o", o, (B, Hq, N, d), (q.dtype,)), ("lse", lse, (B, Hq, N), (torch.float32,)),
+            ("workspace", workspace, None, None))
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    device, stream = _on_device(q, stream)
+    with device:
+        st = load().fa_decode_prefix(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(seq_lens), _ptr(o),
+                                     _ptr(lse), B, Hq, Hkv, N, d, P, max_pages, num_pages, int(prefix_len), float(scale),
+                                     _DTYPES[q.dtype], _ptr(workspace), ws_bytes, _stream(stream))
+    _check(st, where)
+
+
 # ------------------------------------------------------------ conveniences
+
+def _allocating(device, stream):
+    """Context in which buffers of a call on `stream` are allocated and freed
+    in that stream's order."""
+    if stream is None:
+        return torch.cuda.stream(torch.cuda.current_stream(device))
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
+
+
+def cache_append(q, k, v, k_cache, v_cache, block_table, seq_lens, inv_freq=None, new_lens=None,
+                 interleaved: bool = False, stream=None):
+    """Allocates the rotated queries and runs fa_append_paged; returns them
+    (None when q is None).  Rows behind a sequence's new tokens are zero."""
+    q_out = None
+    if q is not None:
+        with _allocating(k.device, stream):
+            make = torch.empty if new_lens is None else torch.zeros
+            q_out = make(q.shape, device=q.device, dtype=q.dtype)
+    fa_append_paged(q, k, v, q_out, None, k_cache, v_cache, block_table, seq_lens, new_lens, inv_freq, interleaved, stream)
+    return q_out
+
+
+def attention_fwd_paged(q, k_cache, v_cache, block_table, seq_lens, new_lens=None, scale: float | None = None,
+                        stream=None):
+    """Allocates O, lse and the workspace and runs fa_fwd_paged.  Rows behind
+    a sequence's new tokens are O = 0, lse = -inf."""
+    B, Hq, N, d = q.shape
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    with _allocating(q.device, stream):
+        if new_lens is None:
+            o = torch.empty_like(q)
+            lse = torch.empty((B, Hq, N), device=q.device, dtype=torch.float32)
+        else:
+            o = torch.zeros_like(q)
+            lse = torch.full((B, Hq, N), -math.inf, device=q.device, dtype=torch.float32)
+        ws = torch.empty(max(fa_fwd_paged_workspace_bytes(B, Hq, k_cache.shape[1], N, d, k_cache.shape[2],
+                                                          block_table.shape[1]), 16),
+                         device=q.device, dtype=torch.uint8)
+    fa_fwd_paged(q, k_cache, v_cache, block_table, seq_lens, new_lens, o, lse, scale, ws, stream)
+    return o, lse
+
+
+def attention_decode_prefix(q, k_cache, v_cache, block_table, seq_lens, prefix_len: int, scale: float | None = None,
+                            stream=None):
+    """Allocates O, lse and the workspace and runs fa_decode_prefix."""
+    B, Hq, Nq, d = q.shape
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    with _allocating(q.device, stream):
+        o = torch.empty_like(q)
+        lse = torch.empty((B, Hq, Nq), device=q.device, dtype=torch.float32)
+        ws = torch.empty(max(fa_decode_prefix_workspace_bytes(B, Hq, k_cache.shape[1], Nq, d, k_cache.shape[2],
+                                                              block_table.shape[1], prefix_len), 16),
+                         device=q.device, dtype=torch.uint8)
+    fa_decode_prefix(q, k_cache, v_cache, block_table, seq_lens, o, lse, scale, prefix_len, ws, stream)
+    return o, lse
+
 
 def attention_decode_paged(q, k_cache, v_cache, block_table, seq_lens, scale: float | None = None,
                            stream=None):

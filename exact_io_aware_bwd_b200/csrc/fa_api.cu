@@ -19,6 +19,8 @@
 #include "fa_fwd_fp8.cuh"
 #include "fa_bwd.cuh"
 #include "fa_decode.cuh"
+#include "fa_append.cuh"
+#include "fa_paged.cuh"
 
 namespace {
 
@@ -152,15 +154,15 @@ fa_status_t opt_in_smem(K kernel, int smem) {
 
 // Launches `kernel` as a programmatic dependent of the kernel before it on the
 // stream: it may be scheduled while that kernel still runs, and waits
-// (griddepcontrol.wait) before it touches global memory.  Used for the decode
-// pair (split, then merge), whose launch gap is a visible part of a step; on
-// the training path it measured slower and is not used.
+// (griddepcontrol.wait) before it touches global memory.  Used on the serving
+// path (cache append, decode), whose launch gaps are a visible part of a step;
+// on the training path it measured slower and is not used.
 template <typename... Params, typename... Args>
-cudaError_t launch_dependent(void (*kernel)(Params...), unsigned grid, unsigned block, int smem,
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, unsigned block, int smem,
                              cudaStream_t st, Args&&... args) {
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = st;
@@ -752,6 +754,177 @@ fa_status_t fa_decode_paged(const void* q, const void* k_cache, const void* v_ca
 #undef FA_DECODE_RB
 #undef FA_DECODE_RUN
   return rs;
+}
+
+}  // extern "C"
+
+namespace {
+
+// Checks shared by the paged-cache entry points (sizes, types, page geometry).
+fa_status_t check_paged(int B, int Hq, int Hkv, int N, int d, int page_size, int max_pages, int num_pages,
+                        fa_dtype_t dtype) {
+  if (B < 0 || N < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || max_pages <= 0 || num_pages <= 0)
+    return FA_ERR_INVALID_ARG;
+  if (dtype != FA_BF16 && dtype != FA_FP16) return FA_ERR_UNSUPPORTED;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128) return FA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(max_pages) * page_size > INT32_MAX - 127 ||
+      static_cast<int64_t>(num_pages) * Hkv > INT32_MAX || static_cast<int64_t>(B) * Hq > INT32_MAX ||
+      static_cast<int64_t>(B) * Hq * N > INT32_MAX)
+    return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+fa_status_t paged_rows(const void* q, const void* k_cache, const void* v_cache, const int* block_table,
+                       const int* seq_lens, const int* new_lens, void* o, float* lse, int B, int Hq, int Hkv,
+                       int N, int d, int page_size, int max_pages, int num_pages, int prefix, float scale,
+                       fa_dtype_t dtype, void* stream) {
+  fa_status_t s = check_device();
+  if (s != FA_OK) return s;
+  fa::PagedParams prm;
+  std::memset(&prm, 0, sizeof(prm));
+  prm.q = q;
+  prm.k_cache = k_cache;
+  prm.v_cache = v_cache;
+  prm.table = block_table;
+  prm.lens = seq_lens;
+  prm.new_lens = new_lens;
+  prm.o = o;
+  prm.lse = lse;
+  prm.rows = static_cast<long long>(B) * Hq * N;
+  prm.Hq = Hq;
+  prm.Hkv = Hkv;
+  prm.N = N;
+  prm.P = page_size;
+  prm.max_pages = max_pages;
+  prm.num_pages = num_pages;
+  prm.prefix = prefix;
+  prm.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const unsigned grid = static_cast<unsigned>((prm.rows + 7) / 8);
+  const bool bf = dtype == FA_BF16;
+  if (d == 128)
+    (bf ? fa::fa_paged_rows_kernel<128, true> : fa::fa_paged_rows_kernel<128, false>)<<<grid, 256, 0, st>>>(prm);
+  else
+    (bf ? fa::fa_paged_rows_kernel<64, true> : fa::fa_paged_rows_kernel<64, false>)<<<grid, 256, 0, st>>>(prm);
+  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+fa_status_t fa_append_paged(const void* q, const void* k, const void* v, const int64_t* strides, void* q_out,
+                            void* k_out, void* k_cache, void* v_cache, const int* block_table,
+                            const int* seq_lens, const int* new_lens, const float* inv_freq, int B, int Hq,
+                            int Hkv, int N, int d, int page_size, int max_pages, int num_pages, int rot_dim,
+                            int interleaved, fa_dtype_t dtype, void* stream) {
+  fa_status_t s = check_paged(B, Hq, Hkv, N, d, page_size, max_pages, num_pages, dtype);
+  if (s != FA_OK) return s;
+  if (rot_dim < 0 || rot_dim > d || (interleaved != 0 && interleaved != 1)) return FA_ERR_INVALID_ARG;
+  if (rot_dim % 16 != 0) return FA_ERR_UNSUPPORTED;
+  if (B == 0 || N == 0) return FA_OK;
+  if (!k || !v || !k_cache || !v_cache || !block_table || !seq_lens || (q == nullptr) != (q_out == nullptr) ||
+      (rot_dim > 0 && !inv_freq))
+    return FA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(k_out) ||
+      !aligned16(k_cache) || !aligned16(v_cache) || !aligned4(block_table) || !aligned4(seq_lens) ||
+      !aligned4(new_lens) || !aligned4(inv_freq))
+    return FA_ERR_MISALIGNED;
+  fa::AppendParams prm;
+  std::memset(&prm, 0, sizeof(prm));
+  for (int i = 0; i < 3; ++i) {
+    const int64_t heads = i == 0 ? Hq : Hkv;
+    const int64_t dense[3] = {heads * N * d, static_cast<int64_t>(N) * d, d};
+    long long* dst = i == 0 ? prm.qs : i == 1 ? prm.ks : prm.vs;
+    for (int j = 0; j < 3; ++j) {
+      dst[j] = strides ? strides[3 * i + j] : dense[j];
+      if (dst[j] % 8 != 0 && (i > 0 || q)) return FA_ERR_MISALIGNED;  // rows start on 16-byte boundaries
+    }
+  }
+  if ((s = check_device()) != FA_OK) return s;
+  prm.q = q;
+  prm.k = k;
+  prm.v = v;
+  prm.q_out = q_out;
+  prm.k_out = k_out;
+  prm.k_cache = k_cache;
+  prm.v_cache = v_cache;
+  prm.table = block_table;
+  prm.lens = seq_lens;
+  prm.new_lens = new_lens;
+  prm.inv_freq = inv_freq;
+  prm.tokens = static_cast<long long>(B) * N;
+  prm.Hq = Hq;
+  prm.Hkv = Hkv;
+  prm.N = N;
+  prm.d = d;
+  prm.P = page_size;
+  prm.max_pages = max_pages;
+  prm.num_pages = num_pages;
+  prm.rot = rot_dim;
+  // tokens of a block: as many as its threads hold (one head lane), fewer
+  // when there are few tokens, so that the heads spread over the threads
+  const int rows = fa::kAppendThreads / (d / 16);
+  int tpb = 1;
+  while (tpb < rows && tpb < prm.tokens) tpb *= 2;
+  prm.tok_per_block = tpb;
+  const unsigned gx = static_cast<unsigned>((prm.tokens + tpb - 1) / tpb);
+  const unsigned gy = 1;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool bf = dtype == FA_BF16;
+  auto kern = bf ? (interleaved ? fa::fa_append_kernel<true, true> : fa::fa_append_kernel<true, false>)
+                 : (interleaved ? fa::fa_append_kernel<false, true> : fa::fa_append_kernel<false, false>);
+  return launch_dependent(kern, dim3(gx, gy), fa::kAppendThreads, 0, st, prm) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+size_t fa_fwd_paged_workspace_bytes(int B, int Hq, int Hkv, int N, int d, int page_size, int max_pages) {
+  return 0;
+}
+
+fa_status_t fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, const int* block_table,
+                         const int* seq_lens, const int* new_lens, void* o, float* lse, int B, int Hq, int Hkv,
+                         int N, int d, int page_size, int max_pages, int num_pages, float scale,
+                         fa_dtype_t dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  fa_status_t s = check_paged(B, Hq, Hkv, N, d, page_size, max_pages, num_pages, dtype);
+  if (s != FA_OK) return s;
+  if (!std::isfinite(scale) || !(scale > 0.f)) return FA_ERR_INVALID_ARG;
+  if (B == 0 || N == 0) return FA_OK;
+  if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !o || !lse) return FA_ERR_INVALID_ARG;
+  const size_t need = fa_fwd_paged_workspace_bytes(B, Hq, Hkv, N, d, page_size, max_pages);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return FA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o) || !aligned16(workspace) ||
+      !aligned4(lse) || !aligned4(block_table) || !aligned4(seq_lens) || !aligned4(new_lens))
+    return FA_ERR_MISALIGNED;
+  return paged_rows(q, k_cache, v_cache, block_table, seq_lens, new_lens, o, lse, B, Hq, Hkv, N, d, page_size,
+                    max_pages, num_pages, 0, scale, dtype, stream);
+}
+
+size_t fa_decode_prefix_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d, int page_size, int max_pages,
+                                        int prefix_len) {
+  return 0;
+}
+
+fa_status_t fa_decode_prefix(const void* q, const void* k_cache, const void* v_cache, const int* block_table,
+                             const int* seq_lens, void* o, float* lse, int B, int Hq, int Hkv, int Nq, int d,
+                             int page_size, int max_pages, int num_pages, int prefix_len, float scale,
+                             fa_dtype_t dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  fa_status_t s = check_paged(B, Hq, Hkv, Nq, d, page_size, max_pages, num_pages, dtype);
+  if (s != FA_OK) return s;
+  if (Nq <= 0 || !std::isfinite(scale) || !(scale > 0.f)) return FA_ERR_INVALID_ARG;
+  if (prefix_len < 0 || prefix_len > max_pages * page_size || prefix_len % page_size != 0) return FA_ERR_INVALID_ARG;
+  if ((Hq / Hkv) * Nq > fa::kDecodeMaxRows) return FA_ERR_UNSUPPORTED;
+  if (B == 0) return FA_OK;
+  if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !o || !lse) return FA_ERR_INVALID_ARG;
+  const size_t need = fa_decode_prefix_workspace_bytes(B, Hq, Hkv, Nq, d, page_size, max_pages, prefix_len);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return FA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o) || !aligned16(workspace) ||
+      !aligned4(lse) || !aligned4(block_table) || !aligned4(seq_lens))
+    return FA_ERR_MISALIGNED;
+  return paged_rows(q, k_cache, v_cache, block_table, seq_lens, nullptr, o, lse, B, Hq, Hkv, Nq, d, page_size,
+                    max_pages, num_pages, prefix_len, scale, dtype, stream);
 }
 
 fa_status_t fa_set_bwd_max_blocks(int max_blocks) {

@@ -253,11 +253,99 @@ fa_status_t fa_decode_paged(const void* q, const void* k_cache, const void* v_ca
                             size_t workspace_bytes, void* stream);
 
 /*
+ * The paged cache's other two sides: filling it, and running many new tokens
+ * against it.  Both share fa_decode_paged's layouts:
+ *   k_cache, v_cache [num_pages][Hkv][page_size][d], block_table
+ *   [B][max_pages] int32, seq_lens [B] int32, all in device memory; key p of
+ *   sequence b is slot p % page_size of page block_table[b][p / page_size].
+ * seq_lens[b] = L counts the sequence's cached tokens, the n = new_lens[b] new
+ * ones of this call among them (new_lens NULL: n = N for every sequence), so
+ * new token t < n sits at position L - n + t.  Tokens t >= n of a padded batch
+ * are neither read nor written.  L = 0 marks an idle sequence: nothing of it
+ * is appended, and its attention rows are O = 0, lse = -inf.
+ * Supported: d in {64, 128}, page_size in {16, 32, 64, 128}, bf16/fp16,
+ * Hq % Hkv == 0, B * Hq * N < 2^31, max_pages * page_size <= 2^31 - 128.
+ * Host-side errors as fa_fwd.  A length
+ * that does not fit (n outside [0, N], L outside [n, max_pages * page_size])
+ * or a block-table entry outside [0, num_pages) that the call meets is
+ * detected on the device (nothing out of range is read or written) and
+ * reported by fa_get_device_status as FA_ERR_INVALID_ARG; such a sequence
+ * appends nothing (a bad entry: nothing on that page) and has O = 0, lse =
+ * -inf (a bad entry: unspecified).  Table entries behind a sequence's last
+ * page are not read, and what the slots behind its last token hold (NaN
+ * included) has no influence.
+ */
+
+/*
+ * Appends keys and values to the cache, keys rotated by their position:
+ * position p turns feature pair i < rot_dim / 2 of k (and of q) by the angle
+ * p * inv_freq[i], taken modulo one turn in 64 bits:
+ *   x' = x cos - y sin,  y' = x sin + y cos
+ * where (x, y) are features (i, i + rot_dim / 2), or (2i, 2i + 1) when
+ * interleaved = 1.  Features from rot_dim on, and v, are copied.  rot_dim is a
+ * multiple of 16 up to d; 0: no rotation, inv_freq may be NULL.
+ *   q [B][Hq][N][d] with q_out [B][Hq][N][d] (both NULL: keys and values only)
+ *   k, v [B][Hkv][N][d]; k_out [B][Hkv][N][d] or NULL: the rotated keys again
+ *   as a dense tensor (the k of fa_fwd for a prompt without cached tokens)
+ *   strides: 9 values in host memory, the batch, head and token strides of q,
+ *   k and v in elements (NULL: dense), multiples of 8 (a row of d features is
+ *   contiguous): rows of a packed projection need no copy.
+ * q_out may be q and k_out may be k where those are dense; apart from that no
+ * output overlaps another tensor of the call, and no two new tokens share a
+ * slot.  One kernel, launched as a programmatic dependent (see
+ * fa_decode_paged); no workspace.
+ */
+fa_status_t fa_append_paged(const void* q, const void* k, const void* v, const int64_t* strides,
+                            void* q_out, void* k_out, void* k_cache, void* v_cache,
+                            const int* block_table, const int* seq_lens, const int* new_lens,
+                            const float* inv_freq, int B, int Hq, int Hkv, int N, int d,
+                            int page_size, int max_pages, int num_pages, int rot_dim,
+                            int interleaved, fa_dtype_t dtype, void* stream);
+
+/*
+ * Forward pass of many new tokens over the cache that already holds them (a
+ * prompt behind a cached prefix, a chunk of a long prompt): new token t of
+ * sequence b sees keys 0 .. L - n + t.
+ *   q [B][Hq][N][d]  o [B][Hq][N][d] (same dtype)  lse [B][Hq][N] fp32
+ * workspace (device, 16-byte aligned) of
+ * fa_fwd_paged_workspace_bytes(B, Hq, Hkv, N, d, page_size, max_pages) bytes
+ * holds partial results; NULL where that is 0.
+ */
+size_t fa_fwd_paged_workspace_bytes(int B, int Hq, int Hkv, int N, int d, int page_size,
+                                    int max_pages);
+fa_status_t fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache,
+                         const int* block_table, const int* seq_lens, const int* new_lens, void* o,
+                         float* lse, int B, int Hq, int Hkv, int N, int d, int page_size,
+                         int max_pages, int num_pages, float scale, fa_dtype_t dtype,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * fa_decode_paged for a batch that shares a prefix: the same result, with the
+ * first prefix_len keys (a multiple of page_size; 0: none) taken once for all
+ * sequences, from the pages block_table[0][0 .. prefix_len / page_size).  The
+ * caller sees to it that these pages hold the prefix of every sequence; the
+ * entries of the other sequences' tables for it are not read.  A sequence
+ * shorter than the prefix sees the part up to its own length.  Limits as
+ * fa_decode_paged ((Hq / Hkv) * Nq <= 32).  The cache's prefix slots all hold
+ * tokens.
+ * workspace (device, 16-byte aligned):
+ * fa_decode_prefix_workspace_bytes(B, Hq, Hkv, Nq, d, page_size, max_pages,
+ * prefix_len) bytes.
+ */
+size_t fa_decode_prefix_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d, int page_size,
+                                        int max_pages, int prefix_len);
+fa_status_t fa_decode_prefix(const void* q, const void* k_cache, const void* v_cache,
+                             const int* block_table, const int* seq_lens, void* o, float* lse,
+                             int B, int Hq, int Hkv, int Nq, int d, int page_size, int max_pages,
+                             int num_pages, int prefix_len, float scale, fa_dtype_t dtype,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Synchronises `stream`, then returns and clears the first device-side error
  * any kernel of this library recorded on the current device since the last
  * call: FA_OK, or FA_ERR_TIMEOUT when a bounded barrier wait ran out (the
  * kernel then skipped its remaining work and its outputs are undefined), or
- * FA_ERR_INVALID_ARG when fa_decode_paged met a bad table entry or length.
+ * FA_ERR_INVALID_ARG when a paged-cache call met a bad table entry or length.
  * Returns FA_ERR_CUDA when the stream itself reports an error.
  */
 fa_status_t fa_get_device_status(void* stream);
