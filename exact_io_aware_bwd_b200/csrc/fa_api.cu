@@ -649,6 +649,104 @@ fa_status_t fa_set_profile_events(int kernel_id, void* start, void* stop) {
   return FA_OK;
 }
 
+}  // extern "C"
+
+namespace {
+
+// The split kernel of decode over the pages from first_page on (partial
+// results into `workspace`) and, unless `splits` takes the launched
+// parameters for another merge, the merge kernel.
+fa_status_t decode_run(const void* q, const void* k_cache, const void* v_cache, const int* block_table,
+                       const int* seq_lens, void* o, float* lse, int B, int Hq, int Hkv, int Nq, int d,
+                       int page_size, int max_pages, int num_pages, float scale, fa_dtype_t dtype, int first_page,
+                       bool idle_ok, void* workspace, void* stream, fa::DecodeParams* splits) {
+  fa::DecodeParams prm;
+  std::memset(&prm, 0, sizeof(prm));
+  prm.q = q;
+  prm.table = block_table;
+  prm.lens = seq_lens;
+  prm.o = o;
+  prm.lse = lse;
+  prm.B = B;
+  prm.Hq = Hq;
+  prm.Hkv = Hkv;
+  prm.Nq = Nq;
+  prm.P = page_size;
+  prm.max_pages = max_pages;
+  prm.num_pages = num_pages;
+  // the caches as [num_pages * Hkv][P][d]: one box = 64 features of the P
+  // rows of one (page, kv head)
+  if (static_cast<int64_t>(num_pages) * Hkv > INT32_MAX) return FA_ERR_UNSUPPORTED;
+  const CUtensorMapDataType tdt = dtype == FA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  if (!make_map(&prm.tm_k, k_cache, tdt, 2, d, page_size, static_cast<uint64_t>(num_pages) * Hkv, 64, page_size) ||
+      !make_map(&prm.tm_v, v_cache, tdt, 2, d, page_size, static_cast<uint64_t>(num_pages) * Hkv, 64, page_size))
+    return FA_ERR_CUDA;
+  prm.first_page = first_page;
+  prm.idle_ok = idle_ok ? 1 : 0;
+  const int pages = max_pages - first_page;
+  prm.S = fa::decode_splits(B, Hkv, d, pages);
+  // a split holds whole tiles of 128 keys
+  const int ppt = fa::kDecodeTile / page_size;
+  prm.pages_per_split = ((pages + prm.S - 1) / prm.S + ppt - 1) / ppt * ppt;
+  prm.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  const int64_t rows = static_cast<int64_t>(B) * Hq * Nq;
+  prm.part_o = static_cast<float*>(workspace);
+  prm.part_ml = prm.part_o + rows * prm.S * d;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool bf = dtype == FA_BF16;
+  const int R = (Hq / Hkv) * Nq;
+  const int rb = R <= 4 ? 4 : R <= 8 ? 8 : R <= 16 ? 16 : 32;
+  // q as [B * Hq * Nq][d]; a box is the NP (rows padded to 16 or 32) rows
+  // that start at an item's first row
+  const int np = rb < 16 ? 16 : rb;
+  if (!make_map(&prm.tm_q, q, tdt, 2, d, static_cast<uint64_t>(B) * Hq * Nq, 1, 64, np)) return FA_ERR_CUDA;
+  const int64_t n_work = static_cast<int64_t>(B) * Hkv * prm.S;
+  if (n_work > INT32_MAX) return FA_ERR_UNSUPPORTED;
+  const int sms = sm_count();
+  if (sms <= 0) return FA_ERR_CUDA;
+  auto run = [&](auto split_kern, auto merge_kern, int smem) -> fa_status_t {
+    fa_status_t r = opt_in_smem(split_kern, smem);
+    if (r != FA_OK) return r;
+    // persistent: as many blocks as fit on the GPU at once, each taking
+    // work items (splits) in turn
+    int per_sm = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, split_kern, fa::kDecodeThreads, smem) !=
+            cudaSuccess ||
+        per_sm <= 0)
+      return FA_ERR_CUDA;
+    const int grid = static_cast<int>(std::min<int64_t>(n_work, static_cast<int64_t>(sms) * per_sm));
+    if (launch_dependent(split_kern, static_cast<unsigned>(grid), fa::kDecodeThreads, smem, st, prm) !=
+        cudaSuccess)
+      return FA_ERR_CUDA;
+    if (splits != nullptr) {
+      *splits = prm;
+      return FA_OK;
+    }
+    return launch_dependent(merge_kern, static_cast<unsigned>(rows), static_cast<unsigned>(d), 0, st, prm) ==
+                   cudaSuccess
+               ? FA_OK
+               : FA_ERR_CUDA;
+  };
+#define FA_DECODE_RUN(HD, BFV, RBV)                                                                  \
+  run(fa::fa_decode_split_kernel<HD, BFV, RBV>, fa::fa_decode_merge_kernel<HD, BFV>, \
+      fa::DecodeLayout<HD, RBV>::kDynSmem)
+#define FA_DECODE_RB(HD, BFV)                                                        \
+  (rb == 4 ? FA_DECODE_RUN(HD, BFV, 4) : rb == 8 ? FA_DECODE_RUN(HD, BFV, 8)        \
+             : rb == 16 ? FA_DECODE_RUN(HD, BFV, 16) : FA_DECODE_RUN(HD, BFV, 32))
+  fa_status_t rs;
+  if (d == 128)
+    rs = bf ? FA_DECODE_RB(128, true) : FA_DECODE_RB(128, false);
+  else
+    rs = bf ? FA_DECODE_RB(64, true) : FA_DECODE_RB(64, false);
+#undef FA_DECODE_RB
+#undef FA_DECODE_RUN
+  return rs;
+}
+
+}  // namespace
+
+extern "C" {
+
 size_t fa_decode_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d, int max_pages) {
   if (B <= 0 || Hq <= 0 || Hkv <= 0 || Nq <= 0 || d <= 0 || max_pages <= 0) return 0;
   return fa::decode_workspace_bytes(B, Hq, Hkv, Nq, d, max_pages);
@@ -680,80 +778,8 @@ fa_status_t fa_decode_paged(const void* q, const void* k_cache, const void* v_ca
     return FA_ERR_MISALIGNED;
   fa_status_t s = check_device();
   if (s != FA_OK) return s;
-  fa::DecodeParams prm;
-  std::memset(&prm, 0, sizeof(prm));
-  prm.q = q;
-  prm.table = block_table;
-  prm.lens = seq_lens;
-  prm.o = o;
-  prm.lse = lse;
-  prm.B = B;
-  prm.Hq = Hq;
-  prm.Hkv = Hkv;
-  prm.Nq = Nq;
-  prm.P = page_size;
-  prm.max_pages = max_pages;
-  prm.num_pages = num_pages;
-  // the caches as [num_pages * Hkv][P][d]: one box = 64 features of the P
-  // rows of one (page, kv head)
-  if (static_cast<int64_t>(num_pages) * Hkv > INT32_MAX) return FA_ERR_UNSUPPORTED;
-  const CUtensorMapDataType tdt = dtype == FA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  if (!make_map(&prm.tm_k, k_cache, tdt, 2, d, page_size, static_cast<uint64_t>(num_pages) * Hkv, 64, page_size) ||
-      !make_map(&prm.tm_v, v_cache, tdt, 2, d, page_size, static_cast<uint64_t>(num_pages) * Hkv, 64, page_size))
-    return FA_ERR_CUDA;
-  prm.S = fa::decode_splits(B, Hkv, d, max_pages);
-  // a split holds whole tiles of 128 keys
-  const int ppt = fa::kDecodeTile / page_size;
-  prm.pages_per_split = ((max_pages + prm.S - 1) / prm.S + ppt - 1) / ppt * ppt;
-  prm.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
-  const int64_t rows = static_cast<int64_t>(B) * Hq * Nq;
-  prm.part_o = static_cast<float*>(workspace);
-  prm.part_ml = prm.part_o + rows * prm.S * d;
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const bool bf = dtype == FA_BF16;
-  const int R = (Hq / Hkv) * Nq;
-  const int rb = R <= 4 ? 4 : R <= 8 ? 8 : R <= 16 ? 16 : 32;
-  // q as [B * Hq * Nq][d]; a box is the NP (rows padded to 16 or 32) rows
-  // that start at an item's first row
-  const int np = rb < 16 ? 16 : rb;
-  if (!make_map(&prm.tm_q, q, tdt, 2, d, static_cast<uint64_t>(B) * Hq * Nq, 1, 64, np)) return FA_ERR_CUDA;
-  const int64_t n_work = static_cast<int64_t>(B) * Hkv * prm.S;
-  if (n_work > INT32_MAX) return FA_ERR_UNSUPPORTED;
-  const int sms = sm_count();
-  if (sms <= 0) return FA_ERR_CUDA;
-  auto run = [&](auto split_kern, auto merge_kern, int smem) -> fa_status_t {
-    fa_status_t r = opt_in_smem(split_kern, smem);
-    if (r != FA_OK) return r;
-    // persistent: as many blocks as fit on the GPU at once, each taking
-    // work items (splits) in turn
-    int per_sm = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, split_kern, fa::kDecodeThreads, smem) !=
-            cudaSuccess ||
-        per_sm <= 0)
-      return FA_ERR_CUDA;
-    const int grid = static_cast<int>(std::min<int64_t>(n_work, static_cast<int64_t>(sms) * per_sm));
-    if (launch_dependent(split_kern, static_cast<unsigned>(grid), fa::kDecodeThreads, smem, st, prm) !=
-        cudaSuccess)
-      return FA_ERR_CUDA;
-    return launch_dependent(merge_kern, static_cast<unsigned>(rows), static_cast<unsigned>(d), 0, st, prm) ==
-                   cudaSuccess
-               ? FA_OK
-               : FA_ERR_CUDA;
-  };
-#define FA_DECODE_RUN(HD, BFV, RBV)                                                                  \
-  run(fa::fa_decode_split_kernel<HD, BFV, RBV>, fa::fa_decode_merge_kernel<HD, BFV>, \
-      fa::DecodeLayout<HD, RBV>::kDynSmem)
-#define FA_DECODE_RB(HD, BFV)                                                        \
-  (rb == 4 ? FA_DECODE_RUN(HD, BFV, 4) : rb == 8 ? FA_DECODE_RUN(HD, BFV, 8)        \
-             : rb == 16 ? FA_DECODE_RUN(HD, BFV, 16) : FA_DECODE_RUN(HD, BFV, 32))
-  fa_status_t rs;
-  if (d == 128)
-    rs = bf ? FA_DECODE_RB(128, true) : FA_DECODE_RB(128, false);
-  else
-    rs = bf ? FA_DECODE_RB(64, true) : FA_DECODE_RB(64, false);
-#undef FA_DECODE_RB
-#undef FA_DECODE_RUN
-  return rs;
+  return decode_run(q, k_cache, v_cache, block_table, seq_lens, o, lse, B, Hq, Hkv, Nq, d, page_size, max_pages,
+                    num_pages, scale, dtype, 0, false, workspace, stream, nullptr);
 }
 
 }  // extern "C"
@@ -777,39 +803,149 @@ fa_status_t check_paged(int B, int Hq, int Hkv, int N, int d, int page_size, int
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
-fa_status_t paged_rows(const void* q, const void* k_cache, const void* v_cache, const int* block_table,
-                       const int* seq_lens, const int* new_lens, void* o, float* lse, int B, int Hq, int Hkv,
-                       int N, int d, int page_size, int max_pages, int num_pages, int prefix, float scale,
-                       fa_dtype_t dtype, void* stream) {
+// How a pass over the paged cache is cut into blocks.
+struct PagedPlan {
+  int toks, seqs;   // a row tile: tokens x sequences (x G heads)
+  int n_tiles;      // row tiles of an owner
+  int64_t owners;   // kv heads, of every sequence in the forward pass
+  int S, S_single;  // key splits of a pair of row tiles / of an odd last one
+  bool joined;      // partial results go through the workspace
+  int slots() const { return std::max(S, S_single); }
+  int64_t rows() const { return owners * n_tiles * 128; }
+  size_t o_bytes(int d) const { return joined ? static_cast<size_t>(rows()) * slots() * d * 4u : 0; }
+  size_t bytes(int d) const { return joined ? o_bytes(d) + static_cast<size_t>(rows()) * slots() * 8u : 0; }
+};
+
+// Splits by a model of the time, in steps of one row tile on one key tile
+// (0.62 us at d = 128, half of a pair's): a block costs its steps and 6 more
+// for its start and end; blocks run in waves of one per SM; joining costs 5
+// steps for the launch and the partial results' way through L2 (a row of a
+// split: 8 d + 16 bytes at 5 TB/s).  Up to a wave of splits, at least 2 key
+// tiles each.
+PagedPlan paged_plan(int B, int Hq, int Hkv, int N, int d, int64_t keys, bool prefix) {
+  PagedPlan pl;
+  const int G = Hq / Hkv;
+  pl.toks = prefix ? N : std::min(N, 128 / G);
+  pl.seqs = prefix ? std::min(B, 128 / (G * N)) : 1;
+  pl.n_tiles = prefix ? (B + pl.seqs - 1) / pl.seqs : (N + pl.toks - 1) / pl.toks;
+  pl.owners = prefix ? Hkv : static_cast<int64_t>(B) * Hkv;
+  const int64_t pairs = pl.n_tiles / 2, odd = pl.n_tiles % 2;
+  const int64_t tiles = std::max<int64_t>(1, (keys + 127) / 128);
+  const int64_t cap = std::min<int64_t>(fa::kDecodeSMs, std::max<int64_t>(1, tiles / 2));
+  double best = 1e300;
+  pl.S = pl.S_single = 1;
+  for (int64_t S = 1; S <= cap; ++S) {
+    const int64_t Ss = odd ? (pairs ? (S + 1) / 2 : S) : 1;
+    const int64_t blocks = pl.owners * (pairs * S + odd * Ss);
+    const double waves = static_cast<double>(blocks) / fa::kDecodeSMs;
+    const double steps = std::max(pairs ? 2.0 * ((tiles + S - 1) / S) : 0.0, odd ? 1.0 * ((tiles + Ss - 1) / Ss) : 0.0);
+    double cost = (waves <= 4 ? std::ceil(waves) : waves) * (steps + 6);
+    if (S > 1 || prefix) cost += 5 + static_cast<double>(pl.rows()) * S * (8.0 * d + 16) / 5e12 / 0.62e-6;
+    if (cost < best) {
+      best = cost;
+      pl.S = static_cast<int>(S);
+      pl.S_single = static_cast<int>(Ss);
+    }
+    if (blocks > 8 * fa::kDecodeSMs) break;  // the GPU is full
+  }
+  if (!pairs) pl.S = pl.S_single;
+  pl.joined = prefix || pl.slots() > 1;
+  return pl;
+}
+
+struct PagedArgs {
+  const void *q, *k_cache, *v_cache;
+  const int *table, *lens, *new_lens;
+  void* o;
+  float* lse;
+  int B, Hq, Hkv, N, d, P, max_pages, num_pages, prefix;
+  float scale;
+  fa_dtype_t dtype;
+};
+
+// The paged kernel and, where its results are joined, the merge kernel;
+// between them the decode kernel over each sequence's own pages when there
+// is a prefix with pages behind it.
+fa_status_t paged_run(const PagedArgs& a, const PagedPlan& pl, void* workspace, void* stream) {
   fa_status_t s = check_device();
   if (s != FA_OK) return s;
-  fa::PagedParams prm;
-  std::memset(&prm, 0, sizeof(prm));
-  prm.q = q;
-  prm.k_cache = k_cache;
-  prm.v_cache = v_cache;
-  prm.table = block_table;
-  prm.lens = seq_lens;
-  prm.new_lens = new_lens;
-  prm.o = o;
-  prm.lse = lse;
-  prm.rows = static_cast<long long>(B) * Hq * N;
-  prm.Hq = Hq;
-  prm.Hkv = Hkv;
-  prm.N = N;
-  prm.P = page_size;
-  prm.max_pages = max_pages;
-  prm.num_pages = num_pages;
-  prm.prefix = prefix;
-  prm.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  const bool bf = a.dtype == FA_BF16;
+  const CUtensorMapDataType dt = bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const unsigned grid = static_cast<unsigned>((prm.rows + 7) / 8);
-  const bool bf = dtype == FA_BF16;
-  if (d == 128)
-    (bf ? fa::fa_paged_rows_kernel<128, true> : fa::fa_paged_rows_kernel<128, false>)<<<grid, 256, 0, st>>>(prm);
-  else
-    (bf ? fa::fa_paged_rows_kernel<64, true> : fa::fa_paged_rows_kernel<64, false>)<<<grid, 256, 0, st>>>(prm);
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  const int G = a.Hq / a.Hkv, d = a.d;
+  fa::PagedMergeParams mp;
+  std::memset(&mp, 0, sizeof(mp));
+  fa::PagedParams& prm = mp.p;
+  auto enc = encode_fn();
+  if (!enc) return FA_ERR_CUDA;
+  const cuuint64_t rb = static_cast<cuuint64_t>(d) * 2;  // bytes of a row
+  const cuuint64_t dims[5] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(G), static_cast<cuuint64_t>(a.N),
+                              static_cast<cuuint64_t>(a.Hkv), static_cast<cuuint64_t>(a.B)};
+  const cuuint64_t strides[4] = {rb * a.N, rb, rb * a.N * G, rb * a.N * a.Hq};
+  const cuuint32_t box[5] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(pl.toks), 1,
+                             static_cast<cuuint32_t>(pl.seqs)};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  if (enc(&prm.tm_q, dt, 5, const_cast<void*>(a.q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return FA_ERR_CUDA;
+  const uint64_t outer = static_cast<uint64_t>(a.num_pages) * a.Hkv;
+  if (!make_map(&prm.tm_k, a.k_cache, dt, 2, d, a.P, outer, 64, a.P) ||
+      !make_map(&prm.tm_v, a.v_cache, dt, 2, d, a.P, outer, 64, a.P))
+    return FA_ERR_CUDA;
+  prm.table = a.table;
+  prm.lens = a.lens;
+  prm.new_lens = a.new_lens;
+  prm.o = a.o;
+  prm.lse = a.lse;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  if (pl.joined) {
+    prm.part_o = reinterpret_cast<float4*>(ws);
+    prm.part_ml = reinterpret_cast<float2*>(ws + pl.o_bytes(d));
+  }
+  prm.B = a.B;
+  prm.Hq = a.Hq;
+  prm.Hkv = a.Hkv;
+  prm.G = G;
+  prm.N = a.N;
+  prm.P = a.P;
+  prm.max_pages = a.max_pages;
+  prm.num_pages = a.num_pages;
+  prm.prefix = a.prefix;
+  prm.toks = pl.toks;
+  prm.seqs = pl.seqs;
+  prm.n_tiles = pl.n_tiles;
+  prm.S = pl.S;
+  prm.S_single = pl.S_single;
+  prm.slots = pl.slots();
+  prm.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
+  const int64_t blocks = pl.owners * (static_cast<int64_t>(pl.n_tiles / 2) * pl.S + (pl.n_tiles % 2) * pl.S_single);
+  if (blocks > INT32_MAX) return FA_ERR_UNSUPPORTED;
+  auto run = [&](auto kern, auto merge, int smem) -> fa_status_t {
+    fa_status_t r = opt_in_smem(kern, smem);
+    if (r != FA_OK) return r;
+    if (launch_dependent(kern, dim3(static_cast<unsigned>(blocks)), fa::kFwdThreads, smem, st, prm) != cudaSuccess)
+      return FA_ERR_CUDA;
+    if (!pl.joined) return FA_OK;
+    const int shared = a.prefix / a.P;
+    if (a.prefix && a.max_pages > shared) {
+      fa::DecodeParams own;
+      r = decode_run(a.q, a.k_cache, a.v_cache, a.table, a.lens, a.o, a.lse, a.B, a.Hq, a.Hkv, a.N, d, a.P,
+                     a.max_pages, a.num_pages, a.scale, a.dtype, shared, true, ws + pl.bytes(d), stream, &own);
+      if (r != FA_OK) return r;
+      mp.own_o = own.part_o;
+      mp.own_ml = own.part_ml;
+      mp.own_S = own.S;
+    }
+    const int64_t grid = pl.rows() / (1024 / d);
+    return launch_dependent(merge, dim3(static_cast<unsigned>(grid)), 256, 0, st, mp) == cudaSuccess ? FA_OK
+                                                                                                   : FA_ERR_CUDA;
+  };
+#define FA_PAGED_RUN(HD, BFV) \
+  run(fa::fa_paged_kernel<HD, BFV>, fa::fa_paged_merge_kernel<HD, BFV>, fa::FwdLayout<HD>::kDynSmem)
+  if (d == 128) return bf ? FA_PAGED_RUN(128, true) : FA_PAGED_RUN(128, false);
+  return bf ? FA_PAGED_RUN(64, true) : FA_PAGED_RUN(64, false);
+#undef FA_PAGED_RUN
 }
 
 }  // namespace
@@ -881,7 +1017,10 @@ fa_status_t fa_append_paged(const void* q, const void* k, const void* v, const i
 }
 
 size_t fa_fwd_paged_workspace_bytes(int B, int Hq, int Hkv, int N, int d, int page_size, int max_pages) {
-  return 0;
+  if (B <= 0 || Hq <= 0 || Hkv <= 0 || N <= 0 || d <= 0 || page_size <= 0 || max_pages <= 0 || Hq % Hkv != 0 ||
+      Hq / Hkv > 128)
+    return 0;
+  return paged_plan(B, Hq, Hkv, N, d, static_cast<int64_t>(max_pages) * page_size, false).bytes(d);
 }
 
 fa_status_t fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, const int* block_table,
@@ -891,20 +1030,28 @@ fa_status_t fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache
   fa_status_t s = check_paged(B, Hq, Hkv, N, d, page_size, max_pages, num_pages, dtype);
   if (s != FA_OK) return s;
   if (!std::isfinite(scale) || !(scale > 0.f)) return FA_ERR_INVALID_ARG;
+  if (Hq / Hkv > 128) return FA_ERR_UNSUPPORTED;
   if (B == 0 || N == 0) return FA_OK;
   if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !o || !lse) return FA_ERR_INVALID_ARG;
-  const size_t need = fa_fwd_paged_workspace_bytes(B, Hq, Hkv, N, d, page_size, max_pages);
-  if (need > 0 && (!workspace || workspace_bytes < need)) return FA_ERR_INVALID_ARG;
+  const PagedPlan pl = paged_plan(B, Hq, Hkv, N, d, static_cast<int64_t>(max_pages) * page_size, false);
+  if (pl.bytes(d) > 0 && (!workspace || workspace_bytes < pl.bytes(d))) return FA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o) || !aligned16(workspace) ||
       !aligned4(lse) || !aligned4(block_table) || !aligned4(seq_lens) || !aligned4(new_lens))
     return FA_ERR_MISALIGNED;
-  return paged_rows(q, k_cache, v_cache, block_table, seq_lens, new_lens, o, lse, B, Hq, Hkv, N, d, page_size,
-                    max_pages, num_pages, 0, scale, dtype, stream);
+  return paged_run({q, k_cache, v_cache, block_table, seq_lens, new_lens, o, lse, B, Hq, Hkv, N, d, page_size,
+                    max_pages, num_pages, 0, scale, dtype},
+                   pl, workspace, stream);
 }
 
 size_t fa_decode_prefix_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d, int page_size, int max_pages,
                                         int prefix_len) {
-  return 0;
+  if (B <= 0 || Hq <= 0 || Hkv <= 0 || Nq <= 0 || d <= 0 || page_size <= 0 || max_pages <= 0 || prefix_len < 0 ||
+      Hq % Hkv != 0 || static_cast<int64_t>(Hq / Hkv) * Nq > fa::kDecodeMaxRows)
+    return 0;
+  if (prefix_len == 0) return fa::decode_workspace_bytes(B, Hq, Hkv, Nq, d, max_pages);
+  const int own = max_pages - prefix_len / page_size;
+  return paged_plan(B, Hq, Hkv, Nq, d, prefix_len, true).bytes(d) +
+         (own > 0 ? fa::decode_workspace_bytes(B, Hq, Hkv, Nq, d, own) : 0);
 }
 
 fa_status_t fa_decode_prefix(const void* q, const void* k_cache, const void* v_cache, const int* block_table,
@@ -915,16 +1062,23 @@ fa_status_t fa_decode_prefix(const void* q, const void* k_cache, const void* v_c
   if (s != FA_OK) return s;
   if (Nq <= 0 || !std::isfinite(scale) || !(scale > 0.f)) return FA_ERR_INVALID_ARG;
   if (prefix_len < 0 || prefix_len > max_pages * page_size || prefix_len % page_size != 0) return FA_ERR_INVALID_ARG;
-  if ((Hq / Hkv) * Nq > fa::kDecodeMaxRows) return FA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(Hq / Hkv) * Nq > fa::kDecodeMaxRows) return FA_ERR_UNSUPPORTED;
   if (B == 0) return FA_OK;
-  if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !o || !lse) return FA_ERR_INVALID_ARG;
-  const size_t need = fa_decode_prefix_workspace_bytes(B, Hq, Hkv, Nq, d, page_size, max_pages, prefix_len);
-  if (need > 0 && (!workspace || workspace_bytes < need)) return FA_ERR_INVALID_ARG;
+  if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !o || !lse || !workspace) return FA_ERR_INVALID_ARG;
+  if (workspace_bytes <
+      fa_decode_prefix_workspace_bytes(B, Hq, Hkv, Nq, d, page_size, max_pages, prefix_len))
+    return FA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o) || !aligned16(workspace) ||
       !aligned4(lse) || !aligned4(block_table) || !aligned4(seq_lens))
     return FA_ERR_MISALIGNED;
-  return paged_rows(q, k_cache, v_cache, block_table, seq_lens, nullptr, o, lse, B, Hq, Hkv, Nq, d, page_size,
-                    max_pages, num_pages, prefix_len, scale, dtype, stream);
+  if (prefix_len == 0) {
+    if ((s = check_device()) != FA_OK) return s;
+    return decode_run(q, k_cache, v_cache, block_table, seq_lens, o, lse, B, Hq, Hkv, Nq, d, page_size, max_pages,
+                      num_pages, scale, dtype, 0, true, workspace, stream, nullptr);
+  }
+  return paged_run({q, k_cache, v_cache, block_table, seq_lens, nullptr, o, lse, B, Hq, Hkv, Nq, d, page_size,
+                    max_pages, num_pages, prefix_len, scale, dtype},
+                   paged_plan(B, Hq, Hkv, Nq, d, prefix_len, true), workspace, stream);
 }
 
 fa_status_t fa_set_bwd_max_blocks(int max_blocks) {

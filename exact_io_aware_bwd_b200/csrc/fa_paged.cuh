@@ -1,75 +1,672 @@
-// Attention of rows of new tokens over a paged key/value cache: the forward
-// pass of many new tokens (fa_fwd_paged) and decode of a batch that shares a
-// prefix (fa_decode_prefix).  One warp per query row, one key at a time.
+// Attention of many query rows over a paged key/value cache: the forward pass
+// of new tokens (fa_fwd_paged) and the prefix part of a decode step whose
+// sequences share their first pages (fa_decode_prefix).  Both are the forward
+// pass's product chain (S = Q K^T, online softmax, O += P V; all in tensor
+// memory) over keys found through a block table; they differ in which rows
+// make up a tile.
+//
+// A row tile is 128 rows of one kv head that see the same keys:
+//   forward   toks = 128 / G consecutive new tokens of one sequence times the
+//             G = Hq / Hkv query heads of the group, token-major, so that a
+//             tile's rows end at nearly the same key and the group's heads
+//             share each key read;
+//   prefix    seqs = 128 / (G N) sequences times their G N rows: the whole
+//             batch reads each prefix key once per 256 rows.
+// Either is one box of a 5-D tensor map over q (feature, head of the group,
+// token, kv head, sequence).
+//
+// A thread block takes two row tiles of a kv head (a pair) or, when the count
+// is odd, the last one alone, and a range of 128-key tiles:
+//   pair      row tile t belongs to softmax warpgroup t, both read every key
+//             tile: step i is row tile i & 1 on key tile i >> 1;
+//   single    both warpgroups hold the same rows and take turns on the key
+//             tiles: step i is warpgroup i & 1 on key tile i; their two
+//             partial results are joined in shared memory at the end.
+// The tensor cores run S_i+2 right after O += P_i V: one warpgroup's softmax
+// overlaps the other's products in both forms.
+//
+// When there are too few blocks to fill the GPU the key tiles of a row tile are
+// split over several blocks, each leaving unnormalised O with its reference
+// max m and sum l (base 2) in the workspace; fa_paged_merge_kernel joins them
+// (and the partial results of each sequence's own keys):
+//   m* = max m_s, l* = sum l_s 2^(m_s - m*), O = sum O_s 2^(m_s - m*) / l*.
+//
+// Warp roles (384 threads) and the register split are those of the forward
+// kernel: softmax warpgroups 0 and 1, MMA warp 8, TMA warp 9.  A key tile is
+// 128 / P page boxes; the TMA warp holds 32 table entries in its lanes, and the
+// lanes of a tile's pages issue its copies side by side.
+//
+// Slots behind a sequence's last token may hold anything, NaN included: scores
+// of hidden keys are replaced, and the value rows of such slots are cleared
+// in shared memory before the product reads them (0 * NaN is not 0).
 #pragma once
 
 #include <type_traits>
 
 #include "fa_decode.cuh"  // programmatic dependent launch, kStatusBadInput
+#include "fa_fwd.cuh"     // FwdLayout, register split, kRefSlack
 
 namespace fa {
 
 constexpr uint32_t kKernPaged = 13;
+constexpr int kPagedTile = 128;  // rows of a row tile, keys of a key tile
 
 struct PagedParams {
-  const void* q;
-  const void* k_cache;
-  const void* v_cache;
-  const int* table;
-  const int* lens;
-  const int* new_lens;
-  void* o;
-  float* lse;
-  long long rows;
-  int Hq, Hkv, N, P, max_pages, num_pages;
-  int prefix;  // keys below it: the pages of sequence 0
+  CUtensorMap tm_q;  // q as (d, G, N, Hkv, B), box 64 x G x toks x 1 x seqs
+  CUtensorMap tm_k;  // [num_pages * Hkv][P][d], box 64 x P
+  CUtensorMap tm_v;
+  const int* table;     // [B][max_pages]
+  const int* lens;      // [B]
+  const int* new_lens;  // [B] or nullptr: N each
+  void* o;              // [B][Hq][N][d], written here when part_o is nullptr
+  float* lse;           // [B][Hq][N]
+  float4* part_o;       // [owner][row tile][slots][d / 4][128]
+  float2* part_ml;      // [owner][row tile][slots][128]: (m, l) in base 2
+  int B, Hq, Hkv, G, N, P, max_pages, num_pages;
+  int prefix;           // keys of the shared prefix; 0: forward pass
+  int toks, seqs;       // a row tile: tokens x sequences (x G heads)
+  int n_tiles;          // row tiles of an owner (kv head, of a sequence in the forward pass)
+  int S, S_single;      // key splits of a pair / of a single
+  int slots;            // the larger of the two
   float scale_log2;
 };
 
+// What a sequence's lengths allow.
+struct PagedSeq {
+  int L, n;     // cached tokens, new tokens
+  int row_end;  // new-token rows that are written
+  bool bad, live;
+};
+
+__device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int b) {
+  PagedSeq q;
+  q.L = p.lens[b];
+  q.n = p.new_lens ? p.new_lens[b] : p.N;
+  const bool n_ok = q.n >= 0 && q.n <= p.N;
+  q.bad = !n_ok || (q.L != 0 && (q.L < q.n || q.L > static_cast<long long>(p.max_pages) * p.P));
+  q.live = !q.bad && q.L > 0;
+  q.row_end = q.bad ? p.N : q.n;
+  return q;
+}
+
+// Row r of a row tile: sequence, token and output row ((b Hq + h) N + token).
+struct PagedRow {
+  int b, t;
+  bool in_tile;
+  long long out;
+};
+
+__device__ __forceinline__ PagedRow paged_row(const PagedParams& p, int owner, int tile, int r) {
+  PagedRow w;
+  const int hg = r % p.G, x = r / p.G;
+  if (p.prefix) {
+    w.b = tile * p.seqs + x / p.N;
+    w.t = x % p.N;
+    w.in_tile = r < p.seqs * p.N * p.G && w.b < p.B;
+  } else {
+    w.b = owner / p.Hkv;
+    w.t = tile * p.toks + x;
+    w.in_tile = r < p.toks * p.G && w.t < p.N;
+  }
+  w.out = (static_cast<long long>(w.b) * p.Hq + (owner % p.Hkv) * p.G + hg) * p.N + w.t;
+  return w;
+}
+
+__device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, uint64_t* bar, int32_t c0, int32_t c1,
+                                            int32_t c2, int32_t c3, int32_t c4) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+      : "memory");
+}
+
 template <int HD, bool BF16>
-__global__ void __launch_bounds__(256) fa_paged_rows_kernel(const __grid_constant__ PagedParams p) {
+__global__ void __launch_bounds__(kFwdThreads, 1) fa_paged_kernel(const __grid_constant__ PagedParams p) {
+  using L = FwdLayout<HD>;
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
-  constexpr int E = HD / 32;
-  const int lane = threadIdx.x & 31;
-  const long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  if (row >= p.rows) return;
-  const int t = static_cast<int>(row % p.N);
-  const int h = static_cast<int>(row / p.N % p.Hq), b = static_cast<int>(row / p.N / p.Hq);
-  const int g = h / (p.Hq / p.Hkv);
-  const int L = p.lens[b];
-  const int n = p.new_lens ? p.new_lens[b] : p.N;
-  const bool bad = n < 0 || n > p.N || L < n || L > static_cast<long long>(p.max_pages) * p.P;
-  if (L != 0 && bad && h == 0 && t == 0 && lane == 0) record_error(kStatusBadInput, kKernPaged, 0, 0);
-  if (p.new_lens && !bad && t >= n) return;
-  const T* q = static_cast<const T*>(p.q) + row * HD;
-  float qv[E], acc[E], m = -INFINITY, l = 0.f;
-  for (int e = 0; e < E; ++e) {
-    qv[e] = static_cast<float>(q[lane * E + e]);
-    acc[e] = 0.f;
-  }
-  const int last = L == 0 || bad ? -1 : L - n + t;
-  for (int key = 0; key <= last; ++key) {
-    const int phys = p.table[(key < p.prefix ? 0 : static_cast<size_t>(b) * p.max_pages) + key / p.P];
-    if (phys < 0 || phys >= p.num_pages) {
-      if (lane == 0) record_error(kStatusBadInput, kKernPaged, 0, 1);
-      continue;
+  constexpr int NS = L::kSlots;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                           ~static_cast<uintptr_t>(1023));
+  uint8_t* sQ = sm + L::kOffQ;
+  uint8_t* sRing = sm + L::kOffRing;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::kOffBar);
+  uint64_t* q_full = bars;
+  uint64_t* slot_full = bars + 1;
+  uint64_t* slot_empty = slot_full + NS;
+  uint64_t* s_full = slot_empty + NS;
+  uint64_t* p_half = s_full + 2;  // [warpgroup][half]
+  uint64_t* pv_done = p_half + 4;
+  uint64_t* done_bar = pv_done + 2;
+  uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(sm + L::kOffTmemPtr);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::kOffAbort);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int box_rows = p.G * p.toks * p.seqs;  // rows of a tile that the q box fills
+
+  if (tid == 0) {
+    mbar_init(q_full, 1);
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&slot_full[s], 1);
+      mbar_init(&slot_empty[s], 1);
     }
-    const long long off = ((static_cast<long long>(phys) * p.Hkv + g) * p.P + key % p.P) * HD + lane * E;
-    const T* k = static_cast<const T*>(p.k_cache) + off;
-    const T* v = static_cast<const T*>(p.v_cache) + off;
-    float s = 0.f;
-    for (int e = 0; e < E; ++e) s += qv[e] * static_cast<float>(k[e]);
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    s *= p.scale_log2;
-    const float mn = fmaxf(m, s);
-    const float w = exp2f(m - mn), x = exp2f(s - mn);
-    m = mn;
-    l = l * w + x;
-    for (int e = 0; e < E; ++e) acc[e] = acc[e] * w + x * static_cast<float>(v[e]);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_half[2 * i], 128);
+      mbar_init(&p_half[2 * i + 1], 128);
+      mbar_init(&pv_done[i], 1);
+    }
+    mbar_init(done_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
   }
-  T* o = static_cast<T*>(p.o) + row * HD;
-  for (int e = 0; e < E; ++e) o[lane * E + e] = static_cast<T>(l > 0.f ? acc[e] / l : 0.f);
-  if (lane == 0) p.lse[row] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+  if (warp == 8) {
+    tmem_alloc(tmem_ptr, 512);
+    tmem_relinquish();
+  }
+  // rows behind the box (128 is no multiple of G toks): zeros, so that their
+  // scores never move a reference
+  for (int i = tid; i < (128 - box_rows) * 8 * 2 * L::kChunks; i += kFwdThreads) {
+    const int box = i / ((128 - box_rows) * 8), k = i % ((128 - box_rows) * 8);
+    *reinterpret_cast<uint4*>(sQ + box * L::kBoxBytes + box_rows * 128 + k * 16) = make_uint4(0u, 0u, 0u, 0u);
+  }
+  fence_proxy_async_smem();
+  grid_dependency_wait();
+  grid_launch_dependents();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_ptr;
+
+  // The block's item.  Pairs first, the last tokens (most keys) of every
+  // sequence first; then the singles, which take half a pair's time.
+  const int owners = p.prefix ? p.Hkv : p.B * p.Hkv;
+  const int n_pairs = p.n_tiles / 2;
+  int x = blockIdx.x;
+  const bool single = x >= n_pairs * owners * p.S;
+  if (single) x -= n_pairs * owners * p.S;
+  const int splits = single ? p.S_single : p.S;
+  const int split = x % splits;
+  const int owner = (x / splits) % owners;
+  const int tile0 = single ? p.n_tiles - 1 : 2 * (n_pairs - 1 - x / (splits * owners));
+  const int g = owner % p.Hkv, b = p.prefix ? 0 : owner / p.Hkv;
+  int keys, valid_end;  // keys some row of the item sees; keys that hold a token
+  bool dead = false;    // only padding rows: nothing is written
+  if (p.prefix) {
+    keys = valid_end = p.prefix;
+  } else {
+    const PagedSeq q = paged_seq(p, b);
+    if (q.bad && tid == 0 && tile0 == 0 && split == 0 && g == 0) record_error(kStatusBadInput, kKernPaged, 0, 0);
+    const int tok0 = tile0 * p.toks, tok1 = min(q.n, tok0 + (single ? 1 : 2) * p.toks);
+    dead = tok0 >= q.row_end;
+    keys = q.live && !dead ? q.L - q.n + tok1 : 0;
+    valid_end = q.L;
+  }
+  const int n_key_tiles = (keys + kPagedTile - 1) / kPagedTile;
+  const int k0 = static_cast<int>(static_cast<long long>(n_key_tiles) * split / splits);
+  const int n_kv = static_cast<int>(static_cast<long long>(n_key_tiles) * (split + 1) / splits) - k0;
+  const int steps = single ? n_kv : 2 * n_kv;
+
+  if (warp >= 8) setmaxnreg_dec<kFwdOtherRegs>();
+  if (warp >= 10) {
+    // idle warps of the third warpgroup
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ producer
+    if (n_kv > 0) {
+      if (lane == 0) {
+        prefetch_tensormap(&p.tm_k);
+        prefetch_tensormap(&p.tm_v);
+        const int tiles = single ? 1 : 2;
+        mbar_expect_tx(q_full, static_cast<uint32_t>(tiles * L::kChunks * box_rows * 128));
+        for (int t = 0; t < tiles; ++t)
+          for (int c = 0; c < L::kChunks; ++c)
+            tma_load_5d(sQ + t * L::kTileBytes + c * L::kBoxBytes, &p.tm_q, q_full, c * 64, 0,
+                        p.prefix ? 0 : (tile0 + t) * p.toks, g, p.prefix ? (tile0 + t) * p.seqs : b);
+      }
+      const int ppt = kPagedTile / p.P;               // pages of a key tile
+      const int pg0 = k0 * ppt;
+      const int n_pages = (valid_end + p.P - 1) / p.P;  // pages that exist
+      const int* row = p.table + static_cast<size_t>(b) * p.max_pages;
+      auto entry = [&](int pg) { return pg < n_pages ? __ldg(row + pg) : -1; };
+      int cur = entry(pg0 + lane), nxt = entry(pg0 + 32 + lane);
+      bool ok = true;
+      int loaded = 0;
+      for (int kt = 0; ok && kt < n_kv; ++kt) {
+        const int rel = kt * ppt;  // pages since pg0; the lanes hold those of its group of 32
+        if (kt > 0 && rel % 32 == 0) {
+          cur = nxt;
+          nxt = entry(pg0 + rel + 32 + lane);
+        }
+        const int phys = __shfl_sync(0xffffffffu, cur, (rel + lane) & 31);
+        int outer = -1;  // outside the tensor: the box reads as zeros
+        if (lane < ppt && pg0 + rel + lane < n_pages) {
+          if (phys >= 0 && phys < p.num_pages)
+            outer = phys * p.Hkv + g;
+          else
+            record_error(kStatusBadInput, kKernPaged, 9, 1);
+        }
+        for (int which = 0; ok && which < 2; ++which) {
+          const int n = 2 * kt + which, s = n % NS;
+          if (n >= NS)
+            ok = __all_sync(0xffffffffu, mbar_wait(&slot_empty[s], ((n / NS) - 1) & 1, abort_flag, kKernPaged, 9, 0));
+          if (!ok) break;
+          if (lane == 0) mbar_expect_tx(&slot_full[s], L::kTileBytes);
+          __syncwarp();
+          if (lane < ppt)
+            for (int c = 0; c < L::kChunks; ++c)
+              tma_load_3d(sRing + s * L::kTileBytes + c * L::kBoxBytes + lane * p.P * 128, which ? &p.tm_v : &p.tm_k,
+                          &slot_full[s], c * 64, 0, outer);
+          loaded = n + 1;
+        }
+      }
+      // the copies in flight land before the block exits (at once, unless a
+      // wait ran out: the MMA warp waits for every tile)
+      mbar_wait_drain(q_full, 0, kKernPaged, 9, 2);
+      for (int n = max(0, loaded - NS); n < loaded; ++n)
+        mbar_wait_drain(&slot_full[n % NS], (n / NS) & 1, kKernPaged, 9, 3);
+    }
+  } else if (warp == 8) {
+    // ------------------------------------------------------------ MMA issuer
+    constexpr uint32_t kIdS = idesc_f16(BF16, 128, 128, false, false);
+    constexpr uint32_t kIdPV = idesc_f16(BF16, 128, HD, false, true);
+    const uint64_t dQ_k = sdesc_sw128(smem_u32(sQ), 16, 1024);
+    const uint64_t dR_k = sdesc_sw128(smem_u32(sRing), 16, 1024);
+    const uint64_t dR_mn = sdesc_sw128(smem_u32(sRing), L::kBoxBytes, 1024);
+    auto wait_all = [&](uint64_t* bar, uint32_t parity, uint32_t site) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, kKernPaged, 8, site));
+    };
+    // ring position of step i's key tile (its value tile is the next one)
+    auto ring = [&](int i) { return 2 * (single ? i : i >> 1); };
+    // the last step that reads a key tile hands its slots back
+    auto last_reader = [&](int i) { return single || (i & 1) != 0; };
+    auto issue_s = [&](int i) -> bool {
+      const int n = ring(i), s = n % NS, t = i & 1;
+      if (!wait_all(&slot_full[s], (n / NS) & 1, 1)) return false;
+      tc_fence_after();
+      const uint32_t qo = single ? 0u : t * L::kTileBytes, ko = s * L::kTileBytes;
+#pragma unroll
+      for (int k = 0; k < HD / 16; ++k) {
+        const uint32_t off = (k >> 2) * L::kBoxBytes + (k & 3) * 32;
+        umma_ss_w(tmem + t * 128, sdesc_add(dQ_k, qo + off), sdesc_add(dR_k, ko + off), kIdS, k > 0);
+      }
+      umma_commit_w(&s_full[t]);
+      if (last_reader(i)) umma_commit_w(&slot_empty[s]);
+      return true;
+    };
+    auto issue_pv = [&](int i) -> bool {
+      const int n = ring(i) + 1, s = n % NS, t = i & 1, j = i >> 1;
+      if (!wait_all(&slot_full[s], (n / NS) & 1, 2)) return false;
+      const uint32_t vo = s * L::kTileBytes;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if (!wait_all(&p_half[2 * t + half], j & 1, 3)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int k = 4 * half; k < 4 * half + 4; ++k)
+          umma_ts_w(tmem + 256 + t * 128, tmem + t * 128 + k * 8, sdesc_add(dR_mn, vo + k * 2048), kIdPV,
+                    (j > 0 || k > 0) ? 1u : 0u);
+      }
+      umma_commit_w(&pv_done[t]);
+      if (last_reader(i)) umma_commit_w(&slot_empty[s]);
+      return true;
+    };
+    if (steps > 0) {
+      bool ok = wait_all(q_full, 0, 0);
+      tc_fence_after();
+      ok = ok && issue_s(0);
+      if (ok && steps > 1) ok = issue_s(1);
+      // S_i+2 overwrites the tensor memory that O += P_i V reads P_i from; the
+      // tensor core runs one thread's MMAs in issue order, so no wait is put
+      // between them
+      for (int i = 0; ok && i < steps; ++i) {
+        ok = issue_pv(i);
+        if (ok && i + 2 < steps) ok = issue_s(i + 2);
+      }
+    }
+    // every MMA this warp issued completes before tensor memory is freed
+    umma_commit_w(done_bar);
+    mbar_wait_drain(done_bar, 0, kKernPaged, 8, 4);
+  } else {
+    setmaxnreg_inc<kFwdSoftmaxRegs>();
+    // ------------------------------------------------------------ softmax
+    const int t = warp >> 2;    // warpgroup
+    const int r = tid & 127;    // row within the tile == tensor-memory lane
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tm_S = tmem + t * 128 + lane_off;
+    const uint32_t tm_O = tmem + 256 + t * 128 + lane_off;
+    const float c_log2 = p.scale_log2;
+    const uint64_t c2 = f2pack(c_log2, c_log2);
+    const int tile = single ? tile0 : tile0 + t;
+    const PagedRow row = paged_row(p, owner, tile, r);
+    // last key the row sees; rows that are not written compute what they
+    // find (a row never reaches another row's result)
+    int lim = INT32_MAX;
+    bool write = row.in_tile && !dead;
+    if (write) {
+      const PagedSeq q = paged_seq(p, row.b);
+      if (q.bad && p.prefix && owner == 0 && split == 0) record_error(kStatusBadInput, kKernPaged, t, 0);
+      lim = q.live ? q.L - q.n + row.t : -1;
+      if (p.prefix && q.live) lim = min(lim, p.prefix - 1);
+      write = row.t < q.row_end;
+    }
+    const bool warp_works = __any_sync(0xffffffffu, write);
+    const int n_mine = single ? (n_kv + 1 - t) / 2 : n_kv;
+    float m_ref = -INFINITY, l_sum = 0.f;
+    bool ok = true;
+    auto load_s = [&](int kv0, uint32_t* s) {
+      tmem_ld32(tm_S + 0, s);
+      tmem_ld32(tm_S + 32, s + 32);
+      tmem_ld32(tm_S + 64, s + 64);
+      tmem_ld32(tm_S + 96, s + 96);
+      tmem_ld_wait();
+      const int last = lim - kv0;  // last visible column
+      if (last < 127) {
+#pragma unroll
+        for (int c = 0; c < 128; ++c)
+          if (c > last) s[c] = __float_as_uint(-INFINITY);
+      }
+    };
+    // P of the 32 keys 32*q4 .. +31 against the reference -m (nm2), packed to
+    // 16 bits in pk[16]; the unrounded values are summed into acc.
+    auto p_chunk = [&](const uint32_t* s, int q4, uint64_t nm2, uint32_t* pk, uint64_t* acc) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int c = q4 * 32 + 2 * i;
+        const uint64_t y = fma2(f2pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), c2, nm2);
+        const uint64_t pp = f2pack(ex2_approx(f2lo(y)), ex2_approx(f2hi(y)));
+        acc[i & 3] = add2(acc[i & 3], pp);
+        pk[i] = pack2<BF16>(f2lo(pp), f2hi(pp));
+      }
+    };
+    auto hand_over = [&](int half) {
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(&p_half[2 * t + half]);
+    };
+    auto sum_acc = [&](const uint64_t* acc) {
+      const uint64_t a = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
+      return f2lo(a) + f2hi(a);
+    };
+    for (int j = 0; j < n_mine; ++j) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&s_full[t], j & 1, abort_flag, kKernPaged, t, 0))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const int kt = single ? 2 * j + t : j;  // key tile of the block's range
+      const int kv0 = (k0 + kt) * kPagedTile;
+      if (kv0 + kPagedTile > valid_end && (single || t == 0)) {
+        // the tile holds slots without a token: thread r clears value row r
+        // if it is one (the first product on this value tile is this
+        // warpgroup's, and waits for the arrivals below)
+        const int n = 2 * kt + 1, s = n % NS;
+        if (!__all_sync(0xffffffffu, mbar_wait(&slot_full[s], (n / NS) & 1, abort_flag, kKernPaged, t, 3))) {
+          ok = false;
+          break;
+        }
+        if (kv0 + r >= valid_end) {
+#pragma unroll
+          for (int c = 0; c < L::kChunks; ++c)
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              *reinterpret_cast<uint4*>(sRing + s * L::kTileBytes + c * L::kBoxBytes + r * 128 + u * 16) =
+                  make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+      }
+      if (!warp_works) {
+        hand_over(0);
+        hand_over(1);
+        continue;
+      }
+      bool done = false;
+      float m_new;
+      {
+        uint32_t s[128];
+        load_s(kv0, s);
+        // row max, eight independent chains of three-input maxima
+        float mx[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mx[i] = fmaxf(__uint_as_float(s[i]), __uint_as_float(s[8 + i]));
+#pragma unroll
+        for (int c = 16; c < 128; c += 16)
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            mx[i] = max3f(mx[i], __uint_as_float(s[c + i]), __uint_as_float(s[c + 8 + i]));
+        m_new = max3f(max3f(mx[0], mx[1], mx[2]), max3f(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * c_log2;
+        if (j == 0) m_ref = m_new;
+        // the exponentials of keys 0-63 against the current reference do not
+        // wait for the vote on the maxima (as in the forward kernel)
+        const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+        const uint64_t nm2 = f2pack(-m_use, -m_use);
+        uint32_t pk0[16], pk1[16];
+        uint64_t acc[4] = {0, 0, 0, 0};
+        p_chunk(s, 0, nm2, pk0, acc);
+        p_chunk(s, 1, nm2, pk1, acc);
+        if (!__any_sync(0xffffffffu, m_new > m_ref + kRefSlack)) {
+          tmem_st16(tm_S + 0, pk0);
+          tmem_st16(tm_S + 16, pk1);
+          hand_over(0);
+          p_chunk(s, 2, nm2, pk0, acc);
+          tmem_st16(tm_S + 32, pk0);
+          p_chunk(s, 3, nm2, pk1, acc);
+          tmem_st16(tm_S + 48, pk1);
+          l_sum += sum_acc(acc);
+          hand_over(1);
+          done = true;
+        }
+      }
+      if (done) continue;
+      // A reference max must move (never in the first tile): O and l are
+      // rescaled once O += P V of the previous tile is done, the tile redone.
+      if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[t], (j - 1) & 1, abort_flag, kKernPaged, t, 1))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const float m_upd = fmaxf(m_ref, m_new);
+      const float corr = m_upd == -INFINITY ? 1.f : ex2_approx(m_ref - m_upd);
+      const uint64_t corr2 = f2pack(corr, corr);
+      m_ref = m_upd;
+      l_sum *= corr;
+#pragma unroll 1
+      for (int c = 0; c < HD; c += 16) {
+        uint32_t o[16];
+        tmem_ld16(tm_O + c, o);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+          const uint64_t v = mul2(f2pack(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), corr2);
+          o[i] = __float_as_uint(f2lo(v));
+          o[i + 1] = __float_as_uint(f2hi(v));
+        }
+        tmem_st16(tm_O + c, o);
+      }
+      {
+        uint32_t s[128];
+        load_s(kv0, s);
+        const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+        const uint64_t nm2 = f2pack(-m_use, -m_use);
+        uint64_t acc[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int q4 = 0; q4 < 4; ++q4) {
+          uint32_t pk[16];
+          p_chunk(s, q4, nm2, pk, acc);
+          tmem_st16(tm_S + q4 * 16, pk);
+          if (q4 == 1) hand_over(0);
+        }
+        l_sum += sum_acc(acc);
+        hand_over(1);
+      }
+    }
+    // ---------------------------------------------------------------- epilogue
+    bool have = ok && n_mine > 0;
+    if (have) have = mbar_wait(&pv_done[t], (n_mine - 1) & 1, abort_flag, kKernPaged, t, 2);
+    have = __all_sync(0xffffffffu, have);
+    if (have) tc_fence_after();
+    if (!have) m_ref = -INFINITY, l_sum = 0.f;
+    auto read_o = [&](int c, uint32_t* v) {
+      if (have) {
+        tmem_ld32(tm_O + c, v);
+        tmem_ld_wait();
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = 0u;
+      }
+    };
+    // a single: warpgroup 1 leaves its half in the ring (every product that
+    // read it is complete once both warpgroups are here), [d / 4][128] float4
+    float4* sO = reinterpret_cast<float4*>(sRing);
+    float2* sML = reinterpret_cast<float2*>(sRing + HD * 128 * 4);
+    float w_own = 1.f, w_other = 0.f;
+    if (single) {
+      named_barrier_sync(1, 256);
+      if (t == 1) {
+        sML[r] = make_float2(m_ref, l_sum);
+#pragma unroll
+        for (int c = 0; c < HD; c += 32) {
+          uint32_t v[32];
+          read_o(c, v);
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            sO[(c / 4 + u) * 128 + r] = make_float4(__uint_as_float(v[4 * u]), __uint_as_float(v[4 * u + 1]),
+                                                    __uint_as_float(v[4 * u + 2]), __uint_as_float(v[4 * u + 3]));
+        }
+      }
+      named_barrier_sync(1, 256);
+      if (t == 0) {
+        const float2 other = sML[r];
+        const float m = fmaxf(m_ref, other.x);
+        if (m != -INFINITY) {
+          w_own = ex2_approx(m_ref - m);
+          w_other = ex2_approx(other.x - m);
+        }
+        l_sum = l_sum * w_own + other.y * w_other;
+        m_ref = m;
+      }
+    }
+    if (!single || t == 0) {
+      const bool seen = l_sum > 0.f;
+      const bool direct = p.part_o == nullptr;
+      if (direct) {
+        const float inv_l = seen ? 1.f / l_sum : 0.f;
+        w_own *= inv_l;
+        w_other *= inv_l;
+      }
+      const long long part = (static_cast<long long>(owner) * p.n_tiles + tile) * p.slots + split;
+#pragma unroll
+      for (int c = 0; c < HD; c += 32) {
+        uint32_t v[32];
+        read_o(c, v);
+        float f[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]) * w_own;
+        if (single) {
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const float4 y = sO[(c / 4 + u) * 128 + r];
+            f[4 * u] += y.x * w_other;
+            f[4 * u + 1] += y.y * w_other;
+            f[4 * u + 2] += y.z * w_other;
+            f[4 * u + 3] += y.w * w_other;
+          }
+        }
+        if (write) {
+          if (direct) {
+            T* orow = reinterpret_cast<T*>(p.o) + row.out * HD + c;
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              *reinterpret_cast<uint4*>(orow + 8 * u) =
+                  make_uint4(pack2<BF16>(f[8 * u], f[8 * u + 1]), pack2<BF16>(f[8 * u + 2], f[8 * u + 3]),
+                             pack2<BF16>(f[8 * u + 4], f[8 * u + 5]), pack2<BF16>(f[8 * u + 6], f[8 * u + 7]));
+          } else if (seen) {
+            // consecutive threads, consecutive float4: whole lines
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              p.part_o[(part * (HD / 4) + c / 4 + u) * 128 + r] =
+                  make_float4(f[4 * u], f[4 * u + 1], f[4 * u + 2], f[4 * u + 3]);
+          }
+        }
+      }
+      if (write) {
+        if (direct)
+          p.lse[row.out] = seen ? (m_ref + __log2f(l_sum)) * 0.69314718055994531f : -INFINITY;
+        else
+          p.part_ml[part * 128 + r] = make_float2(seen ? m_ref : -INFINITY, l_sum);
+      }
+    }
+    tc_fence_before();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the partial results of every row: those of the key splits above and,
+// behind a shared prefix, those of the sequence's own keys (own_o [row][own_S]
+// [d], own_ml, as the decode kernel leaves them).  A block takes 1024 / d
+// consecutive rows of a row tile: thread = (row, 4 features), rows fastest, so that a warp reads 128 bytes of each split's [d / 4][128] block
+// and 64 of each own row.
+struct PagedMergeParams {
+  PagedParams p;
+  const float* own_o;   // nullptr: none
+  const float* own_ml;
+  int own_S;
+};
+
+template <int HD, bool BF16>
+__global__ void __launch_bounds__(256) fa_paged_merge_kernel(const __grid_constant__ PagedMergeParams a) {
+  using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+  const PagedParams& p = a.p;
+  constexpr int kRows = 1024 / HD;  // rows of a block: 8 or 16
+  constexpr int kGroups = 128 / kRows;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int tile_id = blockIdx.x / kGroups;
+  const int r = (blockIdx.x % kGroups) * kRows + threadIdx.x % kRows, c4 = threadIdx.x / kRows;
+  const int owner = tile_id / p.n_tiles, tile = tile_id % p.n_tiles;
+  const PagedRow row = paged_row(p, owner, tile, r);
+  if (!row.in_tile) return;
+  const PagedSeq q = paged_seq(p, row.b);
+  if (row.t >= q.row_end) return;
+  const bool single = (p.n_tiles & 1) && tile == p.n_tiles - 1;
+  const int S = single ? p.S_single : p.S;
+  const long long part = (static_cast<long long>(owner) * p.n_tiles + tile) * p.slots;
+  const float2* ml = p.part_ml + part * 128 + r;
+  const float4* po = p.part_o + (part * (HD / 4) + c4) * 128 + r;
+  const float2* ml2 = reinterpret_cast<const float2*>(a.own_ml) + row.out * a.own_S;
+  const float4* po2 = reinterpret_cast<const float4*>(a.own_o + row.out * a.own_S * HD) + c4;
+  float m = -INFINITY;
+#pragma unroll 8
+  for (int s = 0; s < S; ++s) m = fmaxf(m, ml[s * 128].x);
+#pragma unroll 4
+  for (int s = 0; s < a.own_S; ++s) m = fmaxf(m, ml2[s].x);
+  float l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](float2 x, const float4* src) {
+    if (x.x == -INFINITY) return;  // an empty split
+    const float w = ex2_approx(x.x - m);
+    const float4 y = *src;
+    l += x.y * w;
+    o.x += y.x * w, o.y += y.y * w, o.z += y.z * w, o.w += y.w * w;
+  };
+  if (m != -INFINITY) {
+#pragma unroll 4
+    for (int s = 0; s < S; ++s) add(ml[s * 128], po + static_cast<long long>(s) * (HD / 4) * 128);
+#pragma unroll 4
+    for (int s = 0; s < a.own_S; ++s) add(ml2[s], po2 + s * (HD / 4));
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  uint2 w;
+  w.x = pack2<BF16>(o.x * inv, o.y * inv);
+  w.y = pack2<BF16>(o.z * inv, o.w * inv);
+  *reinterpret_cast<uint2*>(reinterpret_cast<T*>(p.o) + row.out * HD + 4 * c4) = w;
+  if (c4 == 0) p.lse[row.out] = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
 }  // namespace fa

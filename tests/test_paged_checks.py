@@ -105,6 +105,13 @@ def test_decode_prefix_refusals(lib, kw, status):
     assert prefix(lib, **kw) == status
 
 
+def test_a_small_workspace_is_refused(lib):
+    # sizes whose passes are split along the keys
+    kw = dict(B=1, Hq=4, Hkv=2, N=1, d=128, max_pages=4096, num_pages=5000)
+    assert paged(lib, **kw, ws=15) == INVALID and paged(lib, **kw, ptr={8: 0}) == INVALID
+    assert prefix(lib, **kw, prefix=4096, ws=15) == INVALID and prefix(lib, **kw, prefix=4096, ptr={7: 0}) == INVALID
+
+
 def test_empty_problems_are_no_ops(lib):
     none = {i: 0 for i in range(11)}
     assert append(lib, B=0, ptr=none) == binding.FA_OK and append(lib, N=0, ptr=none) == binding.FA_OK
