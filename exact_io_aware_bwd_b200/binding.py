@@ -380,48 +380,92 @@ def fa_decode_paged(q, k_cache, v_cache, block_table, seq_lens, o, lse, scale: f
 
 
 # ------------------------------------------------------------ paged cache
+#
+# These calls run once per layer and token, so their checks are kept to a few
+# microseconds: plain comparisons, one pass over the tensors.
 
-def _on_device(t, stream):
-    """(context that makes t's device current, stream argument): the default
-    stream is the current one of the tensors' device, whichever device is
-    current when the call is made."""
-    return torch.cuda.device(t.device), torch.cuda.current_stream(t.device) if stream is None else stream
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _paged_dims(where, q, k_cache, v_cache, block_table, seq_lens, new_lens=None, heads=None):
-    """Checks of the cache (`heads` kv heads when given), its table and
-    lengths; returns (B, Hq, N, d, P, Hkv, num_pages, max_pages)."""
-    for name, t, dim in (("q", q, 4), ("k_cache", k_cache, 4), ("v_cache", v_cache, 4), ("block_table", block_table, 2),
-                         ("seq_lens", seq_lens, 1)):
+def _dense(t, shape, dtype, dev):
+    return t.shape == shape and t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
+
+
+def _fits(where, dev, *spec):
+    """Says what is wrong: each (name, tensor, shape, dtype) must have the
+    shape and dtype (None: any), a dense layout and CUDA device `dev`; those
+    that a call may leave out pass as None."""
+    for name, t, shape, dtype in spec:
+        if t is None and name in ("new_lens", "q_out", "k_out", "inv_freq", "workspace"):
+            continue
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{where}: {name} must be a tensor")
-        if t.dim() != dim:
-            raise ValueError(f"{where}: {name} must be {dim}-D, got {tuple(t.shape)}")
-    B, Hq, N, d = q.shape
-    num_pages, Hkv, P, _ = k_cache.shape
-    if q.dtype not in _DTYPES:
-        raise TypeError(f"{where}: q has dtype {q.dtype}, expected bfloat16 or float16")
-    if heads is not None and Hkv != heads:
-        raise ValueError(f"{where}: k has {heads} heads, the cache {Hkv}")
-    same, cache, i32 = (q.dtype,), (num_pages, Hkv, P, d), (torch.int32,)
-    _expect(where, ("k_cache", k_cache, cache, same), ("v_cache", v_cache, cache, same),
-            ("block_table", block_table, (B, block_table.shape[1]), i32), ("seq_lens", seq_lens, (B,), i32),
-            ("new_lens", new_lens, (B,), i32))
-    if q.device != k_cache.device:
-        raise ValueError(f"{where}: all tensors must be on one device (q is on {q.device})")
-    return B, Hq, N, d, P, Hkv, num_pages, block_table.shape[1]
+        if shape is not None and t.shape != shape:
+            raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if dtype is not None and t.dtype is not dtype:
+            raise TypeError(f"{where}: {name} has dtype {t.dtype}, expected {dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{where}: {name} must be contiguous")
+        if t.get_device() != dev:
+            if dev < 0 or not t.is_cuda:
+                raise ValueError(f"{where}: {name} must be on a CUDA device")
+            raise ValueError(f"{where}: all tensors must be on one device ({name} is on {t.device})")
+    if dev < 0:
+        raise ValueError(f"{where}: the tensors must be on a CUDA device")
 
 
-def _row_strides(where, name, t, shape, dtype):
+def _four_d(where, *named):
+    for name, t in named:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{where}: {name} must be a tensor")
+        if t.dim() != 4:
+            raise ValueError(f"{where}: {name} must be 4-D, got {tuple(t.shape)}")
+
+
+def _table_width(where, block_table):
+    if not isinstance(block_table, torch.Tensor):
+        raise TypeError(f"{where}: block_table must be a tensor")
+    if block_table.dim() != 2:
+        raise ValueError(f"{where}: block_table must be 2-D, got {tuple(block_table.shape)}")
+    return block_table.shape[1]
+
+
+def _launch(fn, where, dev, stream, args):
+    """fn(*args, stream) with `dev` current; the default stream is the
+    current one of that device, whichever device is current."""
+    if stream is None:
+        stream = _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
+    elif isinstance(stream, torch.cuda.Stream):
+        stream = stream.cuda_stream
+    if dev == torch.cuda.current_device():
+        st = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, stream)
+    if st != FA_OK:
+        raise FaError(st, where)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _row_strides(where, name, t, shape, dtype, dev):
     """(batch, head, token) strides of a [B, H, N, d] tensor whose rows are
     contiguous; a dimension of one entry or none is never stepped over."""
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{where}: {name} has dtype {t.dtype}, expected {dtype}")
-    if t.stride(3) != 1:
+    if t.stride(3) != 1 and shape[3] > 1:
         raise ValueError(f"{where}: the rows of {name} must be contiguous")
-    return [t.stride(i) if t.shape[i] > 1 else 0 for i in range(3)]
+    if dev >= 0 and t.get_device() != dev:
+        raise ValueError(f"{where}: all tensors must be on one device ({name} is on {t.device})")
+    (b, h, n, _), (sb, sh, sn, _) = shape, t.stride()
+    return sb if b > 1 else 0, sh if h > 1 else 0, sn if n > 1 else 0
+
+
+_NineStrides = ctypes.c_int64 * 9
 
 
 def fa_append_paged(q, k, v, q_out, k_out, k_cache, v_cache, block_table, seq_lens, new_lens, inv_freq,
@@ -435,33 +479,77 @@ def fa_append_paged(q, k, v, q_out, k_out, k_cache, v_cache, block_table, seq_le
     where = "fa_append_paged"
     if (q is None) != (q_out is None):
         raise ValueError(f"{where}: q and q_out come together")
-    for name, t in (("k", k), ("v", v)) + ((("q", q),) if q is not None else ()):
-        if not isinstance(t, torch.Tensor) or t.dim() != 4:
-            raise ValueError(f"{where}: {name} must be 4-D [B, H, N, d]")
-    if k.dtype not in _DTYPES:
-        raise TypeError(f"{where}: k has dtype {k.dtype}, expected bfloat16 or float16")
-    B, Hkv, N, d = k.shape
-    Hq = Hkv if q is None else q.shape[1]
-    strides = [0, 0, 0] if q is None else _row_strides(where, "q", q, (B, Hq, N, d), k.dtype)
-    strides = strides + _row_strides(where, "k", k, (B, Hkv, N, d), k.dtype) \
-        + _row_strides(where, "v", v, (B, Hkv, N, d), k.dtype)
-    if inv_freq is not None and (not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1):
-        raise ValueError(f"{where}: inv_freq must be a 1-D tensor")
-    rot = 0 if inv_freq is None else 2 * inv_freq.shape[0]
-    _, _, _, _, P, _, num_pages, max_pages = _paged_dims(where, k, k_cache, v_cache, block_table, seq_lens, new_lens,
-                                                          heads=Hkv)
-    _expect(where, ("k_cache", k_cache, None, None), ("q_out", q_out, (B, Hq, N, d), (k.dtype,)),
-            ("k_out", k_out, (B, Hkv, N, d), (k.dtype,)), ("inv_freq", inv_freq, None, (torch.float32,)))
-    for name, t in (("q", q), ("v", v)):
-        if t is not None and t.device != k.device:
-            raise ValueError(f"{where}: all tensors must be on one device ({name} is on {t.device})")
-    device, stream = _on_device(k, stream)
-    with device:
-        st = load().fa_append_paged(_ptr(q), _ptr(k), _ptr(v), (ctypes.c_int64 * 9)(*strides), _ptr(q_out),
-                                    _ptr(k_out), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(seq_lens),
-                                    _ptr(new_lens), _ptr(inv_freq), B, Hq, Hkv, N, d, P, max_pages, num_pages, rot,
-                                    int(bool(interleaved)), _DTYPES[k.dtype], _stream(stream))
-    _check(st, where)
+    _four_d(where, ("k", k), ("v", v), ("k_cache", k_cache))
+    dt, dev = k.dtype, k.get_device()
+    if dt not in _DTYPES:
+        raise TypeError(f"{where}: k has dtype {dt}, expected bfloat16 or float16")
+    B, Hkv, N, d = kv_shape = k.shape
+    Hq, q_shape = Hkv, None
+    if q is not None:
+        _four_d(where, ("q", q))
+        Hq = q.shape[1]
+        q_shape = (B, Hq, N, d)
+    strides = None
+    if not (k.is_contiguous() and _dense(v, kv_shape, dt, dev) and (q is None or _dense(q, q_shape, dt, dev))):
+        strides = _NineStrides(*([0, 0, 0] if q is None else _row_strides(where, "q", q, q_shape, dt, dev)),
+                               *_row_strides(where, "k", k, kv_shape, dt, dev),
+                               *_row_strides(where, "v", v, kv_shape, dt, dev))
+    rot = 0
+    if inv_freq is not None:
+        if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
+            raise ValueError(f"{where}: inv_freq must be a 1-D tensor")
+        rot = 2 * inv_freq.shape[0]
+    num_pages, Hc, P, _ = k_cache.shape
+    if Hc != Hkv:
+        raise ValueError(f"{where}: k has {Hkv} heads, the cache {Hc}")
+    max_pages = _table_width(where, block_table)
+    i32, cache = torch.int32, (num_pages, Hkv, P, d)
+    try:
+        fine = (dev >= 0 and _dense(k_cache, cache, dt, dev) and _dense(v_cache, cache, dt, dev)
+                and _dense(block_table, (B, max_pages), i32, dev) and _dense(seq_lens, (B,), i32, dev)
+                and (new_lens is None or _dense(new_lens, (B,), i32, dev))
+                and (q is None or _dense(q_out, q_shape, dt, dev)) and (k_out is None or _dense(k_out, kv_shape, dt, dev))
+                and (rot == 0 or _dense(inv_freq, (rot // 2,), torch.float32, dev)))
+    except AttributeError:  # not a tensor
+        fine = False
+    if not fine:
+        _fits(where, dev, ("k_cache", k_cache, cache, dt), ("v_cache", v_cache, cache, dt),
+              ("block_table", block_table, (B, max_pages), i32), ("seq_lens", seq_lens, (B,), i32),
+              ("new_lens", new_lens, (B,), i32), ("q_out", q_out, q_shape, dt), ("k_out", k_out, kv_shape, dt),
+              ("inv_freq", inv_freq, None, torch.float32))
+    _launch((_lib or load()).fa_append_paged, where, dev, stream,
+            (_addr(q), k.data_ptr(), v.data_ptr(), strides, _addr(q_out), _addr(k_out), k_cache.data_ptr(),
+             v_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), _addr(new_lens), _addr(inv_freq), B, Hq,
+             Hkv, N, d, P, max_pages, num_pages, rot, 1 if interleaved else 0, _DTYPES[dt]))
+
+
+def _attention_paged(where, q, k_cache, v_cache, block_table, seq_lens, new_lens, o, lse, workspace):
+    """Checks shared by the attention passes over the cache; returns the
+    device, the library's pointer and size arguments, and the workspace's."""
+    _four_d(where, ("q", q), ("k_cache", k_cache))
+    dt, dev = q.dtype, q.get_device()
+    if dt not in _DTYPES:
+        raise TypeError(f"{where}: q has dtype {dt}, expected bfloat16 or float16")
+    B, Hq, N, d = q_shape = q.shape
+    num_pages, Hkv, P, _ = k_cache.shape
+    max_pages = _table_width(where, block_table)
+    i32, cache = torch.int32, (num_pages, Hkv, P, d)
+    try:
+        fine = (dev >= 0 and q.is_contiguous() and _dense(k_cache, cache, dt, dev) and _dense(v_cache, cache, dt, dev)
+                and _dense(block_table, (B, max_pages), i32, dev) and _dense(seq_lens, (B,), i32, dev)
+                and (new_lens is None or _dense(new_lens, (B,), i32, dev)) and _dense(o, q_shape, dt, dev)
+                and _dense(lse, (B, Hq, N), torch.float32, dev)
+                and (workspace is None or (workspace.is_contiguous() and workspace.get_device() == dev)))
+    except AttributeError:  # not a tensor
+        fine = False
+    if not fine:
+        _fits(where, dev, ("q", q, q_shape, dt), ("k_cache", k_cache, cache, dt), ("v_cache", v_cache, cache, dt),
+              ("block_table", block_table, (B, max_pages), i32), ("seq_lens", seq_lens, (B,), i32),
+              ("new_lens", new_lens, (B,), i32), ("o", o, q_shape, dt), ("lse", lse, (B, Hq, N), torch.float32),
+              ("workspace", workspace, None, None))
+    tensors = (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr())
+    ws = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return dev, tensors, (o.data_ptr(), lse.data_ptr()), (B, Hq, Hkv, N, d, P, max_pages, num_pages), _DTYPES[dt], ws
 
 
 def fa_fwd_paged_workspace_bytes(B: int, Hq: int, Hkv: int, N: int, d: int, page_size: int, max_pages: int) -> int:
@@ -475,16 +563,9 @@ def fa_fwd_paged(q, k_cache, v_cache, block_table, seq_lens, new_lens, o, lse, s
     seq_lens[b] - new_lens[b] + t sees every key up to its own; workspace of
     at least fa_fwd_paged_workspace_bytes(...) bytes."""
     where = "fa_fwd_paged"
-    B, Hq, N, d, P, Hkv, num_pages, max_pages = _paged_dims(where, q, k_cache, v_cache, block_table, seq_lens, new_lens)
-    _expect(where, ("q", q, None, None), ("o", o, (B, Hq, N, d), (q.dtype,)), ("lse", lse, (B, Hq, N), (torch.float32,)),
-            ("workspace", workspace, None, None))
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    device, stream = _on_device(q, stream)
-    with device:
-        st = load().fa_fwd_paged(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(seq_lens), _ptr(new_lens),
-                                 _ptr(o), _ptr(lse), B, Hq, Hkv, N, d, P, max_pages, num_pages, float(scale),
-                                 _DTYPES[q.dtype], _ptr(workspace), ws_bytes, _stream(stream))
-    _check(st, where)
+    dev, ins, outs, sizes, dt, ws = _attention_paged(where, q, k_cache, v_cache, block_table, seq_lens, new_lens, o, lse,
+                                                     workspace)
+    _launch((_lib or load()).fa_fwd_paged, where, dev, stream, (*ins, _addr(new_lens), *outs, *sizes, scale, dt, *ws))
 
 
 def fa_decode_prefix_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, d: int, page_size: int, max_pages: int,
@@ -499,16 +580,9 @@ def fa_decode_prefix(q, k_cache, v_cache, block_table, seq_lens, o, lse, scale: 
     from the pages of sequence 0.  workspace of at least
     fa_decode_prefix_workspace_bytes(...) bytes."""
     where = "fa_decode_prefix"
-    B, Hq, N, d, P, Hkv, num_pages, max_pages = _paged_dims(where, q, k_cache, v_cache, block_table, seq_lens)
-    _expect(where, ("q", q, None, None), ("o", o, (B, Hq, N, d), (q.dtype,)), ("lse", lse, (B, Hq, N), (torch.float32,)),
-            ("workspace", workspace, None, None))
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    device, stream = _on_device(q, stream)
-    with device:
-        st = load().fa_decode_prefix(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(seq_lens), _ptr(o),
-                                     _ptr(lse), B, Hq, Hkv, N, d, P, max_pages, num_pages, int(prefix_len), float(scale),
-                                     _DTYPES[q.dtype], _ptr(workspace), ws_bytes, _stream(stream))
-    _check(st, where)
+    dev, ins, outs, sizes, dt, ws = _attention_paged(where, q, k_cache, v_cache, block_table, seq_lens, None, o, lse,
+                                                     workspace)
+    _launch((_lib or load()).fa_decode_prefix, where, dev, stream, (*ins, *outs, *sizes, prefix_len, scale, dt, *ws))
 
 
 # ------------------------------------------------------------ conveniences

@@ -21,6 +21,7 @@
 #include "fa_decode.cuh"
 #include "fa_append.cuh"
 #include "fa_paged.cuh"
+#include "fa_prefix.cuh"
 
 namespace {
 
@@ -649,104 +650,6 @@ fa_status_t fa_set_profile_events(int kernel_id, void* start, void* stop) {
   return FA_OK;
 }
 
-}  // extern "C"
-
-namespace {
-
-// The split kernel of decode over the pages from first_page on (partial
-// results into `workspace`) and, unless `splits` takes the launched
-// parameters for another merge, the merge kernel.
-fa_status_t decode_run(const void* q, const void* k_cache, const void* v_cache, const int* block_table,
-                       const int* seq_lens, void* o, float* lse, int B, int Hq, int Hkv, int Nq, int d,
-                       int page_size, int max_pages, int num_pages, float scale, fa_dtype_t dtype, int first_page,
-                       bool idle_ok, void* workspace, void* stream, fa::DecodeParams* splits) {
-  fa::DecodeParams prm;
-  std::memset(&prm, 0, sizeof(prm));
-  prm.q = q;
-  prm.table = block_table;
-  prm.lens = seq_lens;
-  prm.o = o;
-  prm.lse = lse;
-  prm.B = B;
-  prm.Hq = Hq;
-  prm.Hkv = Hkv;
-  prm.Nq = Nq;
-  prm.P = page_size;
-  prm.max_pages = max_pages;
-  prm.num_pages = num_pages;
-  // the caches as [num_pages * Hkv][P][d]: one box = 64 features of the P
-  // rows of one (page, kv head)
-  if (static_cast<int64_t>(num_pages) * Hkv > INT32_MAX) return FA_ERR_UNSUPPORTED;
-  const CUtensorMapDataType tdt = dtype == FA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  if (!make_map(&prm.tm_k, k_cache, tdt, 2, d, page_size, static_cast<uint64_t>(num_pages) * Hkv, 64, page_size) ||
-      !make_map(&prm.tm_v, v_cache, tdt, 2, d, page_size, static_cast<uint64_t>(num_pages) * Hkv, 64, page_size))
-    return FA_ERR_CUDA;
-  prm.first_page = first_page;
-  prm.idle_ok = idle_ok ? 1 : 0;
-  const int pages = max_pages - first_page;
-  prm.S = fa::decode_splits(B, Hkv, d, pages);
-  // a split holds whole tiles of 128 keys
-  const int ppt = fa::kDecodeTile / page_size;
-  prm.pages_per_split = ((pages + prm.S - 1) / prm.S + ppt - 1) / ppt * ppt;
-  prm.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
-  const int64_t rows = static_cast<int64_t>(B) * Hq * Nq;
-  prm.part_o = static_cast<float*>(workspace);
-  prm.part_ml = prm.part_o + rows * prm.S * d;
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const bool bf = dtype == FA_BF16;
-  const int R = (Hq / Hkv) * Nq;
-  const int rb = R <= 4 ? 4 : R <= 8 ? 8 : R <= 16 ? 16 : 32;
-  // q as [B * Hq * Nq][d]; a box is the NP (rows padded to 16 or 32) rows
-  // that start at an item's first row
-  const int np = rb < 16 ? 16 : rb;
-  if (!make_map(&prm.tm_q, q, tdt, 2, d, static_cast<uint64_t>(B) * Hq * Nq, 1, 64, np)) return FA_ERR_CUDA;
-  const int64_t n_work = static_cast<int64_t>(B) * Hkv * prm.S;
-  if (n_work > INT32_MAX) return FA_ERR_UNSUPPORTED;
-  const int sms = sm_count();
-  if (sms <= 0) return FA_ERR_CUDA;
-  auto run = [&](auto split_kern, auto merge_kern, int smem) -> fa_status_t {
-    fa_status_t r = opt_in_smem(split_kern, smem);
-    if (r != FA_OK) return r;
-    // persistent: as many blocks as fit on the GPU at once, each taking
-    // work items (splits) in turn
-    int per_sm = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, split_kern, fa::kDecodeThreads, smem) !=
-            cudaSuccess ||
-        per_sm <= 0)
-      return FA_ERR_CUDA;
-    const int grid = static_cast<int>(std::min<int64_t>(n_work, static_cast<int64_t>(sms) * per_sm));
-    if (launch_dependent(split_kern, static_cast<unsigned>(grid), fa::kDecodeThreads, smem, st, prm) !=
-        cudaSuccess)
-      return FA_ERR_CUDA;
-    if (splits != nullptr) {
-      *splits = prm;
-      return FA_OK;
-    }
-    return launch_dependent(merge_kern, static_cast<unsigned>(rows), static_cast<unsigned>(d), 0, st, prm) ==
-                   cudaSuccess
-               ? FA_OK
-               : FA_ERR_CUDA;
-  };
-#define FA_DECODE_RUN(HD, BFV, RBV)                                                                  \
-  run(fa::fa_decode_split_kernel<HD, BFV, RBV>, fa::fa_decode_merge_kernel<HD, BFV>, \
-      fa::DecodeLayout<HD, RBV>::kDynSmem)
-#define FA_DECODE_RB(HD, BFV)                                                        \
-  (rb == 4 ? FA_DECODE_RUN(HD, BFV, 4) : rb == 8 ? FA_DECODE_RUN(HD, BFV, 8)        \
-             : rb == 16 ? FA_DECODE_RUN(HD, BFV, 16) : FA_DECODE_RUN(HD, BFV, 32))
-  fa_status_t rs;
-  if (d == 128)
-    rs = bf ? FA_DECODE_RB(128, true) : FA_DECODE_RB(128, false);
-  else
-    rs = bf ? FA_DECODE_RB(64, true) : FA_DECODE_RB(64, false);
-#undef FA_DECODE_RB
-#undef FA_DECODE_RUN
-  return rs;
-}
-
-}  // namespace
-
-extern "C" {
-
 size_t fa_decode_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d, int max_pages) {
   if (B <= 0 || Hq <= 0 || Hkv <= 0 || Nq <= 0 || d <= 0 || max_pages <= 0) return 0;
   return fa::decode_workspace_bytes(B, Hq, Hkv, Nq, d, max_pages);
@@ -778,8 +681,80 @@ fa_status_t fa_decode_paged(const void* q, const void* k_cache, const void* v_ca
     return FA_ERR_MISALIGNED;
   fa_status_t s = check_device();
   if (s != FA_OK) return s;
-  return decode_run(q, k_cache, v_cache, block_table, seq_lens, o, lse, B, Hq, Hkv, Nq, d, page_size, max_pages,
-                    num_pages, scale, dtype, 0, false, workspace, stream, nullptr);
+  fa::DecodeParams prm;
+  std::memset(&prm, 0, sizeof(prm));
+  prm.q = q;
+  prm.table = block_table;
+  prm.lens = seq_lens;
+  prm.o = o;
+  prm.lse = lse;
+  prm.B = B;
+  prm.Hq = Hq;
+  prm.Hkv = Hkv;
+  prm.Nq = Nq;
+  prm.P = page_size;
+  prm.max_pages = max_pages;
+  prm.num_pages = num_pages;
+  // the caches as [num_pages * Hkv][P][d]: one box = 64 features of the P
+  // rows of one (page, kv head)
+  if (static_cast<int64_t>(num_pages) * Hkv > INT32_MAX) return FA_ERR_UNSUPPORTED;
+  const CUtensorMapDataType tdt = dtype == FA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  if (!make_map(&prm.tm_k, k_cache, tdt, 2, d, page_size, static_cast<uint64_t>(num_pages) * Hkv, 64, page_size) ||
+      !make_map(&prm.tm_v, v_cache, tdt, 2, d, page_size, static_cast<uint64_t>(num_pages) * Hkv, 64, page_size))
+    return FA_ERR_CUDA;
+  prm.S = fa::decode_splits(B, Hkv, d, max_pages);
+  // a split holds whole tiles of 128 keys
+  const int ppt = fa::kDecodeTile / page_size;
+  prm.pages_per_split = ((max_pages + prm.S - 1) / prm.S + ppt - 1) / ppt * ppt;
+  prm.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  const int64_t rows = static_cast<int64_t>(B) * Hq * Nq;
+  prm.part_o = static_cast<float*>(workspace);
+  prm.part_ml = prm.part_o + rows * prm.S * d;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool bf = dtype == FA_BF16;
+  const int R = (Hq / Hkv) * Nq;
+  const int rb = R <= 4 ? 4 : R <= 8 ? 8 : R <= 16 ? 16 : 32;
+  // q as [B * Hq * Nq][d]; a box is the NP (rows padded to 16 or 32) rows
+  // that start at an item's first row
+  const int np = rb < 16 ? 16 : rb;
+  if (!make_map(&prm.tm_q, q, tdt, 2, d, static_cast<uint64_t>(B) * Hq * Nq, 1, 64, np)) return FA_ERR_CUDA;
+  const int64_t n_work = static_cast<int64_t>(B) * Hkv * prm.S;
+  if (n_work > INT32_MAX) return FA_ERR_UNSUPPORTED;
+  const int sms = sm_count();
+  if (sms <= 0) return FA_ERR_CUDA;
+  auto run = [&](auto split_kern, auto merge_kern, int smem) -> fa_status_t {
+    fa_status_t r = opt_in_smem(split_kern, smem);
+    if (r != FA_OK) return r;
+    // persistent: as many blocks as fit on the GPU at once, each taking
+    // work items (splits) in turn
+    int per_sm = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, split_kern, fa::kDecodeThreads, smem) !=
+            cudaSuccess ||
+        per_sm <= 0)
+      return FA_ERR_CUDA;
+    const int grid = static_cast<int>(std::min<int64_t>(n_work, static_cast<int64_t>(sms) * per_sm));
+    if (launch_dependent(split_kern, static_cast<unsigned>(grid), fa::kDecodeThreads, smem, st, prm) !=
+        cudaSuccess)
+      return FA_ERR_CUDA;
+    return launch_dependent(merge_kern, static_cast<unsigned>(rows), static_cast<unsigned>(d), 0, st, prm) ==
+                   cudaSuccess
+               ? FA_OK
+               : FA_ERR_CUDA;
+  };
+#define FA_DECODE_RUN(HD, BFV, RBV)                                                                  \
+  run(fa::fa_decode_split_kernel<HD, BFV, RBV>, fa::fa_decode_merge_kernel<HD, BFV>, \
+      fa::DecodeLayout<HD, RBV>::kDynSmem)
+#define FA_DECODE_RB(HD, BFV)                                                        \
+  (rb == 4 ? FA_DECODE_RUN(HD, BFV, 4) : rb == 8 ? FA_DECODE_RUN(HD, BFV, 8)        \
+             : rb == 16 ? FA_DECODE_RUN(HD, BFV, 16) : FA_DECODE_RUN(HD, BFV, 32))
+  fa_status_t rs;
+  if (d == 128)
+    rs = bf ? FA_DECODE_RB(128, true) : FA_DECODE_RB(128, false);
+  else
+    rs = bf ? FA_DECODE_RB(64, true) : FA_DECODE_RB(64, false);
+#undef FA_DECODE_RB
+#undef FA_DECODE_RUN
+  return rs;
 }
 
 }  // extern "C"
@@ -829,6 +804,11 @@ PagedPlan paged_plan(int B, int Hq, int Hkv, int N, int d, int64_t keys, bool pr
   pl.seqs = prefix ? std::min(B, 128 / (G * N)) : 1;
   pl.n_tiles = prefix ? (B + pl.seqs - 1) / pl.seqs : (N + pl.toks - 1) / pl.toks;
   pl.owners = prefix ? Hkv : static_cast<int64_t>(B) * Hkv;
+  if (prefix && keys == 0) {  // nothing shared: no blocks, no partial results
+    pl.S = pl.S_single = 0;
+    pl.joined = true;
+    return pl;
+  }
   const int64_t pairs = pl.n_tiles / 2, odd = pl.n_tiles % 2;
   const int64_t tiles = std::max<int64_t>(1, (keys + 127) / 128);
   const int64_t cap = std::min<int64_t>(fa::kDecodeSMs, std::max<int64_t>(1, tiles / 2));
@@ -858,14 +838,30 @@ struct PagedArgs {
   const int *table, *lens, *new_lens;
   void* o;
   float* lse;
-  int B, Hq, Hkv, N, d, P, max_pages, num_pages, prefix;
+  int B, Hq, Hkv, N, d, P, max_pages, num_pages;
+  bool decode;  // behind a prefix (of `prefix` keys)
+  int prefix;
   float scale;
   fa_dtype_t dtype;
 };
 
-// The paged kernel and, where its results are joined, the merge kernel;
-// between them the decode kernel over each sequence's own pages when there
-// is a prefix with pages behind it.
+// Splits of each sequence's own keys: one while there are two blocks per SM,
+// else enough for that, of at least 256 keys each (the block's 4 warps take
+// 16 keys at a time).
+int own_splits(int B, int Hkv, int64_t own_keys) {
+  const int64_t items = static_cast<int64_t>(B) * Hkv, slots = 2 * fa::kDecodeSMs;
+  if (items >= slots) return 1;
+  return static_cast<int>(std::max<int64_t>(1, std::min((slots + items - 1) / items, own_keys / 256)));
+}
+
+size_t own_bytes(int B, int Hq, int N, int d, int S) {
+  return S > 1 ? static_cast<size_t>(B) * Hq * N * S * (static_cast<size_t>(d) + 2) * 4u : 0;
+}
+
+// The paged kernel, where there are keys for it (a forward pass, a prefix);
+// behind a prefix the kernel over each sequence's own keys; the merge kernel
+// where the results of several blocks are joined (the own-key kernel does that
+// itself for the prefix's when its own keys are not split).
 fa_status_t paged_run(const PagedArgs& a, const PagedPlan& pl, void* workspace, void* stream) {
   fa_status_t s = check_device();
   if (s != FA_OK) return s;
@@ -875,7 +871,8 @@ fa_status_t paged_run(const PagedArgs& a, const PagedPlan& pl, void* workspace, 
   const int G = a.Hq / a.Hkv, d = a.d;
   fa::PagedMergeParams mp;
   std::memset(&mp, 0, sizeof(mp));
-  fa::PagedParams& prm = mp.p;
+  fa::PagedParams prm;
+  std::memset(&prm, 0, sizeof(prm));
   auto enc = encode_fn();
   if (!enc) return FA_ERR_CUDA;
   const cuuint64_t rb = static_cast<cuuint64_t>(d) * 2;  // bytes of a row
@@ -911,6 +908,7 @@ fa_status_t paged_run(const PagedArgs& a, const PagedPlan& pl, void* workspace, 
   prm.P = a.P;
   prm.max_pages = a.max_pages;
   prm.num_pages = a.num_pages;
+  prm.decode = a.decode ? 1 : 0;
   prm.prefix = a.prefix;
   prm.toks = pl.toks;
   prm.seqs = pl.seqs;
@@ -921,28 +919,45 @@ fa_status_t paged_run(const PagedArgs& a, const PagedPlan& pl, void* workspace, 
   prm.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
   const int64_t blocks = pl.owners * (static_cast<int64_t>(pl.n_tiles / 2) * pl.S + (pl.n_tiles % 2) * pl.S_single);
   if (blocks > INT32_MAX) return FA_ERR_UNSUPPORTED;
-  auto run = [&](auto kern, auto merge, int smem) -> fa_status_t {
+  auto run = [&](auto kern, auto own1, auto own2, auto merge, int smem, int own_smem) -> fa_status_t {
     fa_status_t r = opt_in_smem(kern, smem);
     if (r != FA_OK) return r;
-    if (launch_dependent(kern, dim3(static_cast<unsigned>(blocks)), fa::kFwdThreads, smem, st, prm) != cudaSuccess)
+    if (blocks > 0 && launch_dependent(kern, dim3(static_cast<unsigned>(blocks)), fa::kFwdThreads, smem, st, prm) !=
+                          cudaSuccess)
       return FA_ERR_CUDA;
-    if (!pl.joined) return FA_OK;
-    const int shared = a.prefix / a.P;
-    if (a.prefix && a.max_pages > shared) {
-      fa::DecodeParams own;
-      r = decode_run(a.q, a.k_cache, a.v_cache, a.table, a.lens, a.o, a.lse, a.B, a.Hq, a.Hkv, a.N, d, a.P,
-                     a.max_pages, a.num_pages, a.scale, a.dtype, shared, true, ws + pl.bytes(d), stream, &own);
-      if (r != FA_OK) return r;
-      mp.own_o = own.part_o;
-      mp.own_ml = own.part_ml;
-      mp.own_S = own.S;
+    if (a.decode) {
+      fa::OwnParams op;
+      std::memset(&op, 0, sizeof(op));
+      op.p = prm;
+      op.S = own_splits(a.B, a.Hkv, static_cast<int64_t>(a.max_pages) * a.P - a.prefix);
+      if (op.S > 1) {
+        op.own_o = reinterpret_cast<float*>(ws + pl.bytes(d));
+        op.own_ml = op.own_o + static_cast<size_t>(a.B) * a.Hq * a.N * op.S * d;
+      }
+      op.follows = a.prefix ? 1 : 0;
+      op.q = a.q;
+      op.k_cache = a.k_cache;
+      op.v_cache = a.v_cache;
+      const int64_t items = static_cast<int64_t>(a.B) * a.Hkv * op.S;
+      if (items > INT32_MAX) return FA_ERR_UNSUPPORTED;
+      if (launch_dependent(G * a.N > 16 ? own2 : own1, dim3(static_cast<unsigned>(items)), fa::kOwnThreads, own_smem, st,
+                           op) != cudaSuccess)
+        return FA_ERR_CUDA;
+      if (op.S == 1) return FA_OK;
+      mp.own_o = op.own_o;
+      mp.own_ml = op.own_ml;
+      mp.own_S = op.S;
+    } else if (!pl.joined) {
+      return FA_OK;
     }
+    mp.p = prm;
     const int64_t grid = pl.rows() / (1024 / d);
     return launch_dependent(merge, dim3(static_cast<unsigned>(grid)), 256, 0, st, mp) == cudaSuccess ? FA_OK
                                                                                                    : FA_ERR_CUDA;
   };
 #define FA_PAGED_RUN(HD, BFV) \
-  run(fa::fa_paged_kernel<HD, BFV>, fa::fa_paged_merge_kernel<HD, BFV>, fa::FwdLayout<HD>::kDynSmem)
+  run(fa::fa_paged_kernel<HD, BFV>, fa::fa_prefix_own_kernel<HD, BFV, 1>, fa::fa_prefix_own_kernel<HD, BFV, 2>, \
+      fa::fa_paged_merge_kernel<HD, BFV>, fa::FwdLayout<HD>::kDynSmem, fa::own_smem<HD>())
   if (d == 128) return bf ? FA_PAGED_RUN(128, true) : FA_PAGED_RUN(128, false);
   return bf ? FA_PAGED_RUN(64, true) : FA_PAGED_RUN(64, false);
 #undef FA_PAGED_RUN
@@ -1007,13 +1022,22 @@ fa_status_t fa_append_paged(const void* q, const void* k, const void* v, const i
   int tpb = 1;
   while (tpb < rows && tpb < prm.tokens) tpb *= 2;
   prm.tok_per_block = tpb;
-  const unsigned gx = static_cast<unsigned>((prm.tokens + tpb - 1) / tpb);
-  const unsigned gy = 1;
+  const int64_t gx = (prm.tokens + tpb - 1) / tpb;
+  if (gx > INT32_MAX) return FA_ERR_UNSUPPORTED;
+  // the heads in gy parts: enough blocks for 4 per SM, but no thread with
+  // fewer than kAppendHeads heads while there is a block for each SM
+  const int heads = (q ? Hq : 0) + 2 * Hkv, lanes = rows / tpb;
+  const int sms = sm_count();
+  if (sms <= 0) return FA_ERR_CUDA;
+  const int64_t most = (heads + lanes - 1) / lanes;                                       // one head a thread
+  const int64_t full = std::max<int64_t>(1, most / fa::kAppendHeads);                     // kAppendHeads each
+  const int64_t want = (4ll * sms + gx - 1) / gx, least = (sms + gx - 1) / gx;
+  const int64_t gy = std::min<int64_t>(std::max(std::min(want, full), std::min(least, most)), 65535);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool bf = dtype == FA_BF16;
   auto kern = bf ? (interleaved ? fa::fa_append_kernel<true, true> : fa::fa_append_kernel<true, false>)
                  : (interleaved ? fa::fa_append_kernel<false, true> : fa::fa_append_kernel<false, false>);
-  return launch_dependent(kern, dim3(gx, gy), fa::kAppendThreads, 0, st, prm) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  return launch_dependent(kern, dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), fa::kAppendThreads, 0, st, prm) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 size_t fa_fwd_paged_workspace_bytes(int B, int Hq, int Hkv, int N, int d, int page_size, int max_pages) {
@@ -1039,7 +1063,7 @@ fa_status_t fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache
       !aligned4(lse) || !aligned4(block_table) || !aligned4(seq_lens) || !aligned4(new_lens))
     return FA_ERR_MISALIGNED;
   return paged_run({q, k_cache, v_cache, block_table, seq_lens, new_lens, o, lse, B, Hq, Hkv, N, d, page_size,
-                    max_pages, num_pages, 0, scale, dtype},
+                    max_pages, num_pages, false, 0, scale, dtype},
                    pl, workspace, stream);
 }
 
@@ -1048,10 +1072,8 @@ size_t fa_decode_prefix_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d, i
   if (B <= 0 || Hq <= 0 || Hkv <= 0 || Nq <= 0 || d <= 0 || page_size <= 0 || max_pages <= 0 || prefix_len < 0 ||
       Hq % Hkv != 0 || static_cast<int64_t>(Hq / Hkv) * Nq > fa::kDecodeMaxRows)
     return 0;
-  if (prefix_len == 0) return fa::decode_workspace_bytes(B, Hq, Hkv, Nq, d, max_pages);
-  const int own = max_pages - prefix_len / page_size;
   return paged_plan(B, Hq, Hkv, Nq, d, prefix_len, true).bytes(d) +
-         (own > 0 ? fa::decode_workspace_bytes(B, Hq, Hkv, Nq, d, own) : 0);
+         own_bytes(B, Hq, Nq, d, own_splits(B, Hkv, static_cast<int64_t>(max_pages) * page_size - prefix_len));
 }
 
 fa_status_t fa_decode_prefix(const void* q, const void* k_cache, const void* v_cache, const int* block_table,
@@ -1064,21 +1086,17 @@ fa_status_t fa_decode_prefix(const void* q, const void* k_cache, const void* v_c
   if (prefix_len < 0 || prefix_len > max_pages * page_size || prefix_len % page_size != 0) return FA_ERR_INVALID_ARG;
   if (static_cast<int64_t>(Hq / Hkv) * Nq > fa::kDecodeMaxRows) return FA_ERR_UNSUPPORTED;
   if (B == 0) return FA_OK;
-  if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !o || !lse || !workspace) return FA_ERR_INVALID_ARG;
-  if (workspace_bytes <
-      fa_decode_prefix_workspace_bytes(B, Hq, Hkv, Nq, d, page_size, max_pages, prefix_len))
-    return FA_ERR_INVALID_ARG;
+  if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !o || !lse) return FA_ERR_INVALID_ARG;
+  const PagedPlan pl = paged_plan(B, Hq, Hkv, Nq, d, prefix_len, true);
+  const size_t need = pl.bytes(d) + own_bytes(B, Hq, Nq, d,
+                                              own_splits(B, Hkv, static_cast<int64_t>(max_pages) * page_size - prefix_len));
+  if (need > 0 && (!workspace || workspace_bytes < need)) return FA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o) || !aligned16(workspace) ||
       !aligned4(lse) || !aligned4(block_table) || !aligned4(seq_lens))
     return FA_ERR_MISALIGNED;
-  if (prefix_len == 0) {
-    if ((s = check_device()) != FA_OK) return s;
-    return decode_run(q, k_cache, v_cache, block_table, seq_lens, o, lse, B, Hq, Hkv, Nq, d, page_size, max_pages,
-                      num_pages, scale, dtype, 0, true, workspace, stream, nullptr);
-  }
   return paged_run({q, k_cache, v_cache, block_table, seq_lens, nullptr, o, lse, B, Hq, Hkv, Nq, d, page_size,
-                    max_pages, num_pages, prefix_len, scale, dtype},
-                   paged_plan(B, Hq, Hkv, Nq, d, prefix_len, true), workspace, stream);
+                    max_pages, num_pages, true, prefix_len, scale, dtype},
+                   pl, workspace, stream);
 }
 
 fa_status_t fa_set_bwd_max_blocks(int max_blocks) {

@@ -29,6 +29,7 @@ namespace fa {
 
 constexpr uint32_t kKernAppend = 12;
 constexpr int kAppendThreads = 256;
+constexpr int kAppendHeads = 4;  // heads whose loads a thread has in flight
 
 struct AppendParams {
   const void* q;  // nullptr: keys and values only
@@ -83,6 +84,26 @@ __global__ void __launch_bounds__(kAppendThreads) fa_append_kernel(const __grid_
   const bool turned = INTER ? 16 * s < p.rot : 8 * s < half;
   const int c0 = INTER || !turned ? 16 * s : 8 * s;
   const int c1 = INTER || !turned ? c0 + 8 : c0 + half;
+
+  const T* q = static_cast<const T*>(p.q) + b * p.qs[0] + t * p.qs[2];
+  const T* k = static_cast<const T*>(p.k) + b * p.ks[0] + t * p.ks[2];
+  const T* v = static_cast<const T*>(p.v) + b * p.vs[0] + t * p.vs[2];
+  const int Hq = p.q ? p.Hq : 0;
+  const int heads = Hq + 2 * p.Hkv;  // query heads, then key heads, then value heads
+  const int step = gridDim.y * head_lanes;
+  int h = blockIdx.y * head_lanes + row / p.tok_per_block;
+  auto load = [&](int hh, uint4& a, uint4& c) {
+    if (hh >= heads) return;
+    const T* src = hh < Hq ? q + hh * p.qs[1] : hh < Hq + p.Hkv ? k + (hh - Hq) * p.ks[1] : v + (hh - Hq - p.Hkv) * p.vs[1];
+    a = *reinterpret_cast<const uint4*>(src + c0);
+    c = *reinterpret_cast<const uint4*>(src + c1);
+  };
+  // kAppendHeads heads in flight at a time; the first ones are asked for
+  // before the sines and cosines are computed
+  uint4 a[kAppendHeads], c[kAppendHeads];
+#pragma unroll
+  for (int u = 0; u < kAppendHeads; ++u) load(h + u * step, a[u], c[u]);
+
   float cs[8], sn[8];
   if (turned) {
 #pragma unroll
@@ -91,61 +112,65 @@ __global__ void __launch_bounds__(kAppendThreads) fa_append_kernel(const __grid_
       sincospif(2.f * static_cast<float>(turns - rint(turns)), &sn[i], &cs[i]);
     }
   }
-
-  const T* q = static_cast<const T*>(p.q);
-  const T* k = static_cast<const T*>(p.k);
-  const T* v = static_cast<const T*>(p.v);
-  const int Hq = q ? p.Hq : 0;
-  const int heads = Hq + 2 * p.Hkv;
-  for (int h = blockIdx.y * head_lanes + row / p.tok_per_block; h < heads; h += gridDim.y * head_lanes) {
-    const bool is_q = h < Hq, is_v = h >= Hq + p.Hkv;
-    const int g = is_q ? h : is_v ? h - Hq - p.Hkv : h - Hq;
-    const T* src = is_q ? q + b * p.qs[0] + g * p.qs[1] + t * p.qs[2]
-                 : is_v ? v + b * p.vs[0] + g * p.vs[1] + t * p.vs[2]
-                        : k + b * p.ks[0] + g * p.ks[1] + t * p.ks[2];
-    uint4 a = *reinterpret_cast<const uint4*>(src + c0), c = *reinterpret_cast<const uint4*>(src + c1);
-    if (turned && !is_v) {
-      T2* a2 = reinterpret_cast<T2*>(&a);
-      T2* c2 = reinterpret_cast<T2*>(&c);
-      float x[8], y[8];
+  auto turn = [&](uint4& av, uint4& cv) {
+    const T2* a2 = reinterpret_cast<const T2*>(&av);
+    const T2* c2 = reinterpret_cast<const T2*>(&cv);
+    float x[8], y[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        // pairs 2i, 2i + 1 (half split: a holds the x, c the y) or, when
-        // interleaved, pair i from a and pair 4 + i from c
-        const float2 u = make_float2(static_cast<float>(a2[i].x), static_cast<float>(a2[i].y));
-        const float2 w = make_float2(static_cast<float>(c2[i].x), static_cast<float>(c2[i].y));
-        if (INTER) {
-          x[i] = u.x, y[i] = u.y, x[4 + i] = w.x, y[4 + i] = w.y;
-        } else {
-          x[2 * i] = u.x, x[2 * i + 1] = u.y, y[2 * i] = w.x, y[2 * i + 1] = w.y;
-        }
-      }
-      uint32_t* aw = reinterpret_cast<uint32_t*>(&a);
-      uint32_t* cw = reinterpret_cast<uint32_t*>(&c);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float xi = x[i], yi = y[i];
-        x[i] = xi * cs[i] - yi * sn[i];
-        y[i] = xi * sn[i] + yi * cs[i];
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        aw[i] = INTER ? pack2<BF16>(x[i], y[i]) : pack2<BF16>(x[2 * i], x[2 * i + 1]);
-        cw[i] = INTER ? pack2<BF16>(x[4 + i], y[4 + i]) : pack2<BF16>(y[2 * i], y[2 * i + 1]);
+    for (int i = 0; i < 4; ++i) {
+      // half split: a holds the x of pairs 2i, 2i + 1, c their y;
+      // interleaved: a holds pair i, c pair 4 + i
+      const float2 u = make_float2(static_cast<float>(a2[i].x), static_cast<float>(a2[i].y));
+      const float2 w = make_float2(static_cast<float>(c2[i].x), static_cast<float>(c2[i].y));
+      if (INTER) {
+        x[i] = u.x, y[i] = u.y, x[4 + i] = w.x, y[4 + i] = w.y;
+      } else {
+        x[2 * i] = u.x, x[2 * i + 1] = u.y, y[2 * i] = w.x, y[2 * i + 1] = w.y;
       }
     }
-    auto put = [&](void* base, long long r) {
-      T* dst = static_cast<T*>(base) + r * p.d;
-      *reinterpret_cast<uint4*>(dst + c0) = a;
-      *reinterpret_cast<uint4*>(dst + c1) = c;
-    };
-    if (is_q) {
-      put(p.q_out, (static_cast<long long>(b) * p.Hq + g) * p.N + t);
-    } else {
-      if (page_ok)
-        put(is_v ? p.v_cache : p.k_cache, (static_cast<long long>(phys) * p.Hkv + g) * p.P + pos % p.P);
-      if (!is_v && p.k_out) put(p.k_out, (static_cast<long long>(b) * p.Hkv + g) * p.N + t);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float xi = x[i], yi = y[i];
+      x[i] = xi * cs[i] - yi * sn[i];
+      y[i] = xi * sn[i] + yi * cs[i];
     }
+    uint32_t aw[4], cw[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      aw[i] = INTER ? pack2<BF16>(x[i], y[i]) : pack2<BF16>(x[2 * i], x[2 * i + 1]);
+      cw[i] = INTER ? pack2<BF16>(x[4 + i], y[4 + i]) : pack2<BF16>(y[2 * i], y[2 * i + 1]);
+    }
+    av = make_uint4(aw[0], aw[1], aw[2], aw[3]);
+    cv = make_uint4(cw[0], cw[1], cw[2], cw[3]);
+  };
+  // this token's rows of head 0; a head further is N (outputs) or P (cache) rows
+  const long long slot = static_cast<long long>(phys) * p.Hkv * p.P + pos % p.P;
+  T* q_out = static_cast<T*>(p.q_out) + (static_cast<long long>(b) * p.Hq * p.N + t) * p.d;
+  T* k_out = static_cast<T*>(p.k_out) + (static_cast<long long>(b) * p.Hkv * p.N + t) * p.d;
+  auto put = [&](T* dst, const uint4& av, const uint4& cv) {
+    *reinterpret_cast<uint4*>(dst + c0) = av;
+    *reinterpret_cast<uint4*>(dst + c1) = cv;
+  };
+  auto store = [&](int hh, uint4& av, uint4& cv) {
+    if (hh >= heads) return;
+    if (turned && hh < Hq + p.Hkv) turn(av, cv);
+    if (hh < Hq) {
+      put(q_out + static_cast<long long>(hh) * p.N * p.d, av, cv);
+    } else if (hh < Hq + p.Hkv) {
+      const long long g = hh - Hq;
+      if (page_ok) put(static_cast<T*>(p.k_cache) + (slot + g * p.P) * p.d, av, cv);
+      if (p.k_out) put(k_out + g * p.N * p.d, av, cv);
+    } else if (page_ok) {
+      put(static_cast<T*>(p.v_cache) + (slot + static_cast<long long>(hh - Hq - p.Hkv) * p.P) * p.d, av, cv);
+    }
+  };
+  for (;;) {
+#pragma unroll
+    for (int u = 0; u < kAppendHeads; ++u) store(h + u * step, a[u], c[u]);
+    h += kAppendHeads * step;
+    if (h >= heads) break;
+#pragma unroll
+    for (int u = 0; u < kAppendHeads; ++u) load(h + u * step, a[u], c[u]);
   }
 }
 

@@ -62,8 +62,6 @@ struct DecodeParams {
   void* o;                // [B][Hq][Nq][d]
   float* lse;             // [B][Hq][Nq]
   int B, Hq, Hkv, Nq, P, max_pages, num_pages, S, pages_per_split;
-  int first_page;         // the splits cover the pages from this one on
-  int idle_ok;            // a sequence of length 0 is no error
   float scale_log2;
 };
 
@@ -179,8 +177,7 @@ __device__ __forceinline__ DecodeItem decode_item(const DecodeParams& p, int w) 
   it.Lb = p.lens[it.b];
   it.len_ok = it.Lb >= p.Nq && it.Lb <= p.max_pages * P;
   const int n_pages = it.len_ok ? (it.Lb + P - 1) / P : 0;
-  if (p.idle_ok && it.Lb == 0) it.len_ok = true;
-  it.pg0 = p.first_page + it.split * p.pages_per_split;  // pages_per_split is a multiple of ppt
+  it.pg0 = it.split * p.pages_per_split;  // pages_per_split is a multiple of ppt
   it.pg1 = min(n_pages, it.pg0 + p.pages_per_split);
   it.n_tiles = it.pg1 > it.pg0 ? (it.pg1 - it.pg0 + ppt - 1) / ppt : 0;
   return it;
@@ -492,18 +489,6 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) fa_decode_split_kernel(cons
 #pragma unroll
         for (int r = 0; r < RB; ++r)
           if (r < R) *reinterpret_cast<T*>(pb + r * 128 + ((((i & 63) >> 3) ^ (r & 7)) << 4)) = static_cast<T>(pr[r]);
-        // Slots behind the sequence's last token may hold anything: their
-        // value rows (this thread's key) are cleared, since the product
-        // V^T P^T would carry a NaN past P = 0.  (The tile has landed: its S
-        // product, which waited for it, is complete.)
-        if (key >= I.Lb) {
-          uint8_t* vrow = sm + (j % NS) * L::kSlotBytes + i * 128;
-#pragma unroll
-          for (int c = 0; c < L::kChunks; ++c)
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-              *reinterpret_cast<uint4*>(vrow + c * L::kChunkBytes + u * 16) = make_uint4(0u, 0u, 0u, 0u);
-        }
         fence_proxy_async_smem();
         tc_fence_before();
         mbar_arrive(&p_full[buf]);

@@ -63,7 +63,8 @@ struct PagedParams {
   float4* part_o;       // [owner][row tile][slots][d / 4][128]
   float2* part_ml;      // [owner][row tile][slots][128]: (m, l) in base 2
   int B, Hq, Hkv, G, N, P, max_pages, num_pages;
-  int prefix;           // keys of the shared prefix; 0: forward pass
+  int decode;           // 1: decode behind a prefix (a tile's rows come from several sequences); 0: forward pass
+  int prefix;           // keys of the shared prefix
   int toks, seqs;       // a row tile: tokens x sequences (x G heads)
   int n_tiles;          // row tiles of an owner (kv head, of a sequence in the forward pass)
   int S, S_single;      // key splits of a pair / of a single
@@ -99,7 +100,7 @@ struct PagedRow {
 __device__ __forceinline__ PagedRow paged_row(const PagedParams& p, int owner, int tile, int r) {
   PagedRow w;
   const int hg = r % p.G, x = r / p.G;
-  if (p.prefix) {
+  if (p.decode) {
     w.b = tile * p.seqs + x / p.N;
     w.t = x % p.N;
     w.in_tile = r < p.seqs * p.N * p.G && w.b < p.B;
@@ -181,7 +182,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_paged_kernel(const __grid_c
 
   // The block's item.  Pairs first, the last tokens (most keys) of every
   // sequence first; then the singles, which take half a pair's time.
-  const int owners = p.prefix ? p.Hkv : p.B * p.Hkv;
+  const int owners = p.decode ? p.Hkv : p.B * p.Hkv;
   const int n_pairs = p.n_tiles / 2;
   int x = blockIdx.x;
   const bool single = x >= n_pairs * owners * p.S;
@@ -190,10 +191,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_paged_kernel(const __grid_c
   const int split = x % splits;
   const int owner = (x / splits) % owners;
   const int tile0 = single ? p.n_tiles - 1 : 2 * (n_pairs - 1 - x / (splits * owners));
-  const int g = owner % p.Hkv, b = p.prefix ? 0 : owner / p.Hkv;
+  const int g = owner % p.Hkv, b = p.decode ? 0 : owner / p.Hkv;
   int keys, valid_end;  // keys some row of the item sees; keys that hold a token
   bool dead = false;    // only padding rows: nothing is written
-  if (p.prefix) {
+  if (p.decode) {
     keys = valid_end = p.prefix;
   } else {
     const PagedSeq q = paged_seq(p, b);
@@ -222,7 +223,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_paged_kernel(const __grid_c
         for (int t = 0; t < tiles; ++t)
           for (int c = 0; c < L::kChunks; ++c)
             tma_load_5d(sQ + t * L::kTileBytes + c * L::kBoxBytes, &p.tm_q, q_full, c * 64, 0,
-                        p.prefix ? 0 : (tile0 + t) * p.toks, g, p.prefix ? (tile0 + t) * p.seqs : b);
+                        p.decode ? 0 : (tile0 + t) * p.toks, g, p.decode ? (tile0 + t) * p.seqs : b);
       }
       const int ppt = kPagedTile / p.P;               // pages of a key tile
       const int pg0 = k0 * ppt;
@@ -345,9 +346,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_paged_kernel(const __grid_c
     bool write = row.in_tile && !dead;
     if (write) {
       const PagedSeq q = paged_seq(p, row.b);
-      if (q.bad && p.prefix && owner == 0 && split == 0) record_error(kStatusBadInput, kKernPaged, t, 0);
       lim = q.live ? q.L - q.n + row.t : -1;
-      if (p.prefix && q.live) lim = min(lim, p.prefix - 1);
+      if (p.decode && q.live) lim = min(lim, p.prefix - 1);
       write = row.t < q.row_end;
     }
     const bool warp_works = __any_sync(0xffffffffu, write);
