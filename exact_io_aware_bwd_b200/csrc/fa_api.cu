@@ -846,12 +846,12 @@ struct PagedArgs {
 };
 
 // Splits of each sequence's own keys: one while there are two blocks per SM,
-// else enough for that, of at least 256 keys each (the block's 4 warps take
-// 16 keys at a time).
+// else enough for that, of at least 1024 keys each (joining them takes another
+// kernel, about the time of 1024 keys).
 int own_splits(int B, int Hkv, int64_t own_keys) {
   const int64_t items = static_cast<int64_t>(B) * Hkv, slots = 2 * fa::kDecodeSMs;
   if (items >= slots) return 1;
-  return static_cast<int>(std::max<int64_t>(1, std::min((slots + items - 1) / items, own_keys / 256)));
+  return static_cast<int>(std::max<int64_t>(1, std::min((slots + items - 1) / items, own_keys / 1024)));
 }
 
 size_t own_bytes(int B, int Hq, int N, int d, int S) {
@@ -919,7 +919,7 @@ fa_status_t paged_run(const PagedArgs& a, const PagedPlan& pl, void* workspace, 
   prm.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
   const int64_t blocks = pl.owners * (static_cast<int64_t>(pl.n_tiles / 2) * pl.S + (pl.n_tiles % 2) * pl.S_single);
   if (blocks > INT32_MAX) return FA_ERR_UNSUPPORTED;
-  auto run = [&](auto kern, auto own1, auto own2, auto merge, int smem, int own_smem) -> fa_status_t {
+  auto run = [&](auto kern, auto own1, auto own2, auto merge, int smem) -> fa_status_t {
     fa_status_t r = opt_in_smem(kern, smem);
     if (r != FA_OK) return r;
     if (blocks > 0 && launch_dependent(kern, dim3(static_cast<unsigned>(blocks)), fa::kFwdThreads, smem, st, prm) !=
@@ -936,12 +936,15 @@ fa_status_t paged_run(const PagedArgs& a, const PagedPlan& pl, void* workspace, 
       }
       op.follows = a.prefix ? 1 : 0;
       op.q = a.q;
-      op.k_cache = a.k_cache;
-      op.v_cache = a.v_cache;
+      if (!make_map(&op.tm_k, a.k_cache, dt, 2, d, a.P, outer, 64, 16) ||
+          !make_map(&op.tm_v, a.v_cache, dt, 2, d, a.P, outer, 64, 16))
+        return FA_ERR_CUDA;
+      const int own_smem = fa::own_smem(G * a.N, op.S == 1 ? pl.slots() : 0);
+      auto own = G * a.N > 16 ? own2 : own1;
+      if ((r = opt_in_smem(own, std::max(own_smem, fa::own_smem(32, fa::kDecodeSMs)))) != FA_OK) return r;
       const int64_t items = static_cast<int64_t>(a.B) * a.Hkv * op.S;
       if (items > INT32_MAX) return FA_ERR_UNSUPPORTED;
-      if (launch_dependent(G * a.N > 16 ? own2 : own1, dim3(static_cast<unsigned>(items)), fa::kOwnThreads, own_smem, st,
-                           op) != cudaSuccess)
+      if (launch_dependent(own, dim3(static_cast<unsigned>(items)), fa::kOwnThreads, own_smem, st, op) != cudaSuccess)
         return FA_ERR_CUDA;
       if (op.S == 1) return FA_OK;
       mp.own_o = op.own_o;
@@ -957,7 +960,7 @@ fa_status_t paged_run(const PagedArgs& a, const PagedPlan& pl, void* workspace, 
   };
 #define FA_PAGED_RUN(HD, BFV) \
   run(fa::fa_paged_kernel<HD, BFV>, fa::fa_prefix_own_kernel<HD, BFV, 1>, fa::fa_prefix_own_kernel<HD, BFV, 2>, \
-      fa::fa_paged_merge_kernel<HD, BFV>, fa::FwdLayout<HD>::kDynSmem, fa::own_smem<HD>())
+      fa::fa_paged_merge_kernel<HD, BFV>, fa::FwdLayout<HD>::kDynSmem)
   if (d == 128) return bf ? FA_PAGED_RUN(128, true) : FA_PAGED_RUN(128, false);
   return bf ? FA_PAGED_RUN(64, true) : FA_PAGED_RUN(64, false);
 #undef FA_PAGED_RUN

@@ -32,9 +32,9 @@
 //   m* = max m_s, l* = sum l_s 2^(m_s - m*), O = sum O_s 2^(m_s - m*) / l*.
 //
 // Warp roles (384 threads) and the register split are those of the forward
-// kernel: softmax warpgroups 0 and 1, MMA warp 8, TMA warp 9.  A key tile is
-// 128 / P page boxes; the TMA warp holds 32 table entries in its lanes, and the
-// lanes of a tile's pages issue its copies side by side.
+// kernel: softmax warpgroups 0 and 1, MMA warp 8, TMA warps 9 (K) and 10 (V).
+// A key tile is 128 / P page boxes; a TMA warp holds 32 table entries in its
+// lanes, and the lanes of a tile's pages issue its copies side by side.
 //
 // Slots behind a sequence's last token may hold anything, NaN included: scores
 // of hidden keys are replaced, and the value rows of such slots are cleared
@@ -113,6 +113,53 @@ __device__ __forceinline__ PagedRow paged_row(const PagedParams& p, int owner, i
   return w;
 }
 
+// One block's work.
+struct PagedItem {
+  bool single;  // one row tile, its key tiles shared out between the warpgroups
+  bool dead;    // only padding rows: nothing is written
+  int split, owner, tile0, g, b;
+  int valid_end;  // keys that hold a token
+  int k0, n_kv;   // key tiles
+};
+
+// Pairs first, the last tokens (most keys) of every sequence first; then the
+// singles, which take half a pair's time.
+__device__ __forceinline__ PagedItem paged_item(const PagedParams& p) {
+  PagedItem it;
+  const int owners = p.decode ? p.Hkv : p.B * p.Hkv;
+  const int n_pairs = p.n_tiles / 2;
+  int x = blockIdx.x;
+  it.single = x >= n_pairs * owners * p.S;
+  if (it.single) x -= n_pairs * owners * p.S;
+  const int splits = it.single ? p.S_single : p.S;
+  it.split = x % splits;
+  it.owner = (x / splits) % owners;
+  it.tile0 = it.single ? p.n_tiles - 1 : 2 * (n_pairs - 1 - x / (splits * owners));
+  it.g = it.owner % p.Hkv;
+  it.b = p.decode ? 0 : it.owner / p.Hkv;
+  it.dead = false;
+  int keys;  // keys some row of the item sees
+  if (p.decode) {
+    keys = it.valid_end = p.prefix;
+  } else {
+    const PagedSeq q = paged_seq(p, it.b);
+    const int tok0 = it.tile0 * p.toks, tok1 = min(q.n, tok0 + (it.single ? 1 : 2) * p.toks);
+    if (q.bad && threadIdx.x == 0 && it.split == 0 && it.g == 0) record_error(kStatusBadInput, kKernPaged, 0, 0);
+    it.dead = tok0 >= q.row_end;
+    keys = q.live && !it.dead ? q.L - q.n + tok1 : 0;
+    it.valid_end = q.L;
+  }
+  const int n = (keys + kPagedTile - 1) / kPagedTile;
+  it.k0 = static_cast<int>(static_cast<long long>(n) * it.split / splits);
+  it.n_kv = static_cast<int>(static_cast<long long>(n) * (it.split + 1) / splits) - it.k0;
+  return it;
+}
+
+// Arrives on a named barrier without waiting for it.
+__device__ __forceinline__ void named_barrier_arrive(uint32_t id, uint32_t count) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+
 __device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, uint64_t* bar, int32_t c0, int32_t c1,
                                             int32_t c2, int32_t c3, int32_t c4) {
   asm volatile(
@@ -146,126 +193,129 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_paged_kernel(const __grid_c
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int box_rows = p.G * p.toks * p.seqs;  // rows of a tile that the q box fills
 
-  if (tid == 0) {
-    mbar_init(q_full, 1);
-    for (int s = 0; s < NS; ++s) {
-      mbar_init(&slot_full[s], 1);
-      mbar_init(&slot_empty[s], 1);
+  // The third warpgroup gives its registers up at once, so that the softmax
+  // warpgroups need not wait for them behind the first loads.
+  if (warp >= 8) setmaxnreg_dec<kFwdOtherRegs>();
+  // ------------------------------------------------------------ producers
+  // Warp 9 loads K tiles (and q), warp 10 V tiles, the first ones before the
+  // block's other warps are set up.
+  const bool produces = warp == 9 || warp == 10;
+  const int which = warp - 9;
+  const int ppt = kPagedTile / p.P;  // pages of a key tile
+  PagedItem it = {};
+  int cur = -1, nxt = -1;  // table entries of 32 pages, one a lane, and of the next 32
+  auto entry = [&](int rel) {  // of the page `rel` after the item's first
+    const int pg = it.k0 * ppt + rel;
+    return pg < (it.valid_end + p.P - 1) / p.P ? __ldg(p.table + static_cast<size_t>(it.b) * p.max_pages + pg) : -1;
+  };
+  auto load_tile = [&](int kt) -> bool {
+    const int rel = kt * ppt;
+    if (kt > 0 && rel % 32 == 0) {
+      cur = nxt;
+      nxt = entry(rel + 32 + lane);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_half[2 * i], 128);
-      mbar_init(&p_half[2 * i + 1], 128);
-      mbar_init(&pv_done[i], 1);
+    const int phys = __shfl_sync(0xffffffffu, cur, (rel + lane) & 31);
+    int outer = -1;  // outside the tensor: the box reads as zeros
+    if (lane < ppt && (it.k0 * ppt + rel + lane) * p.P < it.valid_end) {
+      if (phys >= 0 && phys < p.num_pages)
+        outer = phys * p.Hkv + it.g;
+      else
+        record_error(kStatusBadInput, kKernPaged, 9, 1);
     }
-    mbar_init(done_bar, 1);
-    *abort_flag = 0;
-    fence_mbar_init();
-  }
-  if (warp == 8) {
+    const int n = 2 * kt + which, s = n % NS;
+    if (n >= NS && !__all_sync(0xffffffffu, mbar_wait(&slot_empty[s], ((n / NS) - 1) & 1, abort_flag, kKernPaged, warp, 0)))
+      return false;
+    if (lane == 0) mbar_expect_tx(&slot_full[s], L::kTileBytes);
+    __syncwarp();
+    if (lane < ppt)
+      for (int c = 0; c < L::kChunks; ++c)
+        tma_load_3d(sRing + s * L::kTileBytes + c * L::kBoxBytes + lane * p.P * 128, which ? &p.tm_v : &p.tm_k,
+                    &slot_full[s], c * 64, 0, outer);
+    return true;
+  };
+  // tiles whose slot is empty from the start
+  const int early = (NS - which + 1) / 2;
+
+  if (produces) {
+    if (warp == 9 && lane == 0) {
+      mbar_init(q_full, 1);
+      for (int s = 0; s < NS; ++s) {
+        mbar_init(&slot_full[s], 1);
+        mbar_init(&slot_empty[s], 1);
+      }
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&s_full[i], 1);
+        mbar_init(&p_half[2 * i], 128);
+        mbar_init(&p_half[2 * i + 1], 128);
+        mbar_init(&pv_done[i], 1);
+      }
+      mbar_init(done_bar, 1);
+      *abort_flag = 0;
+      fence_mbar_init();
+    }
+    if (lane == 0) prefetch_tensormap(which ? &p.tm_v : &p.tm_k);
+    named_barrier_sync(2, 64);
+    named_barrier_arrive(3, kFwdThreads);  // the others wait for the barriers, not for the first loads
+    grid_dependency_wait();
+    it = paged_item(p);
+    grid_launch_dependents();
+    if (it.n_kv > 0) {
+      cur = entry(lane);
+      nxt = entry(32 + lane);
+      for (int kt = 0; kt < early && kt < it.n_kv; ++kt) {
+        load_tile(kt);
+        if (warp == 9 && kt == 0 && lane == 0) {
+          const int tiles = it.single ? 1 : 2;
+          mbar_expect_tx(q_full, static_cast<uint32_t>(tiles * L::kChunks * box_rows * 128));
+          for (int t = 0; t < tiles; ++t)
+            for (int c = 0; c < L::kChunks; ++c)
+              tma_load_5d(sQ + t * L::kTileBytes + c * L::kBoxBytes, &p.tm_q, q_full, c * 64, 0,
+                          p.decode ? 0 : (it.tile0 + t) * p.toks, it.g, p.decode ? (it.tile0 + t) * p.seqs : it.b);
+        }
+        __syncwarp();
+      }
+    }
+  } else if (warp == 8) {
     tmem_alloc(tmem_ptr, 512);
     tmem_relinquish();
-  }
-  // rows behind the box (128 is no multiple of G toks): zeros, so that their
-  // scores never move a reference
-  for (int i = tid; i < (128 - box_rows) * 8 * 2 * L::kChunks; i += kFwdThreads) {
-    const int box = i / ((128 - box_rows) * 8), k = i % ((128 - box_rows) * 8);
-    *reinterpret_cast<uint4*>(sQ + box * L::kBoxBytes + box_rows * 128 + k * 16) = make_uint4(0u, 0u, 0u, 0u);
-  }
-  fence_proxy_async_smem();
-  grid_dependency_wait();
-  grid_launch_dependents();
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_ptr;
-
-  // The block's item.  Pairs first, the last tokens (most keys) of every
-  // sequence first; then the singles, which take half a pair's time.
-  const int owners = p.decode ? p.Hkv : p.B * p.Hkv;
-  const int n_pairs = p.n_tiles / 2;
-  int x = blockIdx.x;
-  const bool single = x >= n_pairs * owners * p.S;
-  if (single) x -= n_pairs * owners * p.S;
-  const int splits = single ? p.S_single : p.S;
-  const int split = x % splits;
-  const int owner = (x / splits) % owners;
-  const int tile0 = single ? p.n_tiles - 1 : 2 * (n_pairs - 1 - x / (splits * owners));
-  const int g = owner % p.Hkv, b = p.decode ? 0 : owner / p.Hkv;
-  int keys, valid_end;  // keys some row of the item sees; keys that hold a token
-  bool dead = false;    // only padding rows: nothing is written
-  if (p.decode) {
-    keys = valid_end = p.prefix;
   } else {
-    const PagedSeq q = paged_seq(p, b);
-    if (q.bad && tid == 0 && tile0 == 0 && split == 0 && g == 0) record_error(kStatusBadInput, kKernPaged, 0, 0);
-    const int tok0 = tile0 * p.toks, tok1 = min(q.n, tok0 + (single ? 1 : 2) * p.toks);
-    dead = tok0 >= q.row_end;
-    keys = q.live && !dead ? q.L - q.n + tok1 : 0;
-    valid_end = q.L;
+    // rows behind the box (128 is no multiple of G toks): zeros, so that
+    // their scores never move a reference
+    const int i0 = warp < 8 ? tid : tid - 96;
+    for (int i = i0; i < (128 - box_rows) * 8 * 2 * L::kChunks; i += 288) {
+      const int box = i / ((128 - box_rows) * 8), k = i % ((128 - box_rows) * 8);
+      *reinterpret_cast<uint4*>(sQ + box * L::kBoxBytes + box_rows * 128 + k * 16) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    fence_proxy_async_smem();
   }
-  const int n_key_tiles = (keys + kPagedTile - 1) / kPagedTile;
-  const int k0 = static_cast<int>(static_cast<long long>(n_key_tiles) * split / splits);
-  const int n_kv = static_cast<int>(static_cast<long long>(n_key_tiles) * (split + 1) / splits) - k0;
+  if (!produces) {
+    grid_dependency_wait();
+    it = paged_item(p);
+    tc_fence_before();
+    named_barrier_sync(3, kFwdThreads);
+    tc_fence_after();
+  }
+  const uint32_t tmem = produces ? 0u : *tmem_ptr;
+  const bool single = it.single, dead = it.dead;
+  const int k0 = it.k0, n_kv = it.n_kv, valid_end = it.valid_end, owner = it.owner, split = it.split;
   const int steps = single ? n_kv : 2 * n_kv;
 
-  if (warp >= 8) setmaxnreg_dec<kFwdOtherRegs>();
-  if (warp >= 10) {
-    // idle warps of the third warpgroup
-  } else if (warp == 9) {
-    // ------------------------------------------------------------ producer
+  if (warp == 11) {
+    // idle
+  } else if (produces) {
+    bool ok = true;
+    int kt = early;
+    for (; ok && kt < n_kv; ++kt) ok = load_tile(kt);
+    // the copies in flight land before the block exits (at once, unless a
+    // wait ran out: the MMA warp waits for every tile)
     if (n_kv > 0) {
-      if (lane == 0) {
-        prefetch_tensormap(&p.tm_k);
-        prefetch_tensormap(&p.tm_v);
-        const int tiles = single ? 1 : 2;
-        mbar_expect_tx(q_full, static_cast<uint32_t>(tiles * L::kChunks * box_rows * 128));
-        for (int t = 0; t < tiles; ++t)
-          for (int c = 0; c < L::kChunks; ++c)
-            tma_load_5d(sQ + t * L::kTileBytes + c * L::kBoxBytes, &p.tm_q, q_full, c * 64, 0,
-                        p.decode ? 0 : (tile0 + t) * p.toks, g, p.decode ? (tile0 + t) * p.seqs : b);
+      if (warp == 9) mbar_wait_drain(q_full, 0, kKernPaged, 9, 2);
+      const int loaded = min(ok ? kt : kt - 1, n_kv);
+      for (int k = max(0, loaded - early); k < loaded; ++k) {
+        const int n = 2 * k + which;
+        if (n + NS >= 2 * n_kv)  // else the slot was filled again: it had landed
+          mbar_wait_drain(&slot_full[n % NS], (n / NS) & 1, kKernPaged, warp, 3);
       }
-      const int ppt = kPagedTile / p.P;               // pages of a key tile
-      const int pg0 = k0 * ppt;
-      const int n_pages = (valid_end + p.P - 1) / p.P;  // pages that exist
-      const int* row = p.table + static_cast<size_t>(b) * p.max_pages;
-      auto entry = [&](int pg) { return pg < n_pages ? __ldg(row + pg) : -1; };
-      int cur = entry(pg0 + lane), nxt = entry(pg0 + 32 + lane);
-      bool ok = true;
-      int loaded = 0;
-      for (int kt = 0; ok && kt < n_kv; ++kt) {
-        const int rel = kt * ppt;  // pages since pg0; the lanes hold those of its group of 32
-        if (kt > 0 && rel % 32 == 0) {
-          cur = nxt;
-          nxt = entry(pg0 + rel + 32 + lane);
-        }
-        const int phys = __shfl_sync(0xffffffffu, cur, (rel + lane) & 31);
-        int outer = -1;  // outside the tensor: the box reads as zeros
-        if (lane < ppt && pg0 + rel + lane < n_pages) {
-          if (phys >= 0 && phys < p.num_pages)
-            outer = phys * p.Hkv + g;
-          else
-            record_error(kStatusBadInput, kKernPaged, 9, 1);
-        }
-        for (int which = 0; ok && which < 2; ++which) {
-          const int n = 2 * kt + which, s = n % NS;
-          if (n >= NS)
-            ok = __all_sync(0xffffffffu, mbar_wait(&slot_empty[s], ((n / NS) - 1) & 1, abort_flag, kKernPaged, 9, 0));
-          if (!ok) break;
-          if (lane == 0) mbar_expect_tx(&slot_full[s], L::kTileBytes);
-          __syncwarp();
-          if (lane < ppt)
-            for (int c = 0; c < L::kChunks; ++c)
-              tma_load_3d(sRing + s * L::kTileBytes + c * L::kBoxBytes + lane * p.P * 128, which ? &p.tm_v : &p.tm_k,
-                          &slot_full[s], c * 64, 0, outer);
-          loaded = n + 1;
-        }
-      }
-      // the copies in flight land before the block exits (at once, unless a
-      // wait ran out: the MMA warp waits for every tile)
-      mbar_wait_drain(q_full, 0, kKernPaged, 9, 2);
-      for (int n = max(0, loaded - NS); n < loaded; ++n)
-        mbar_wait_drain(&slot_full[n % NS], (n / NS) & 1, kKernPaged, 9, 3);
     }
   } else if (warp == 8) {
     // ------------------------------------------------------------ MMA issuer
@@ -315,14 +365,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_paged_kernel(const __grid_c
     if (steps > 0) {
       bool ok = wait_all(q_full, 0, 0);
       tc_fence_after();
-      ok = ok && issue_s(0);
-      if (ok && steps > 1) ok = issue_s(1);
-      // S_i+2 overwrites the tensor memory that O += P_i V reads P_i from; the
-      // tensor core runs one thread's MMAs in issue order, so no wait is put
-      // between them
-      for (int i = 0; ok && i < steps; ++i) {
-        ok = issue_pv(i);
-        if (ok && i + 2 < steps) ok = issue_s(i + 2);
+      // S_0 S_1 | P_0 V, S_2 | P_1 V, S_3 | ...  S_i+2 overwrites the tensor
+      // memory that O += P_i V reads P_i from; the tensor core runs one
+      // thread's MMAs in issue order, so no wait is put between them.  (One
+      // copy of each in the code: a cold instruction line costs microseconds
+      // while every block's first loads are in flight.)
+      for (int i = 0; ok && i < steps + 2; ++i) {
+        if (i >= 2) ok = issue_pv(i - 2);
+        if (ok && i < steps) ok = issue_s(i);
       }
     }
     // every MMA this warp issued completes before tensor memory is freed
@@ -338,7 +388,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_paged_kernel(const __grid_c
     const uint32_t tm_O = tmem + 256 + t * 128 + lane_off;
     const float c_log2 = p.scale_log2;
     const uint64_t c2 = f2pack(c_log2, c_log2);
-    const int tile = single ? tile0 : tile0 + t;
+    const int tile = single ? it.tile0 : it.tile0 + t;
     const PagedRow row = paged_row(p, owner, tile, r);
     // last key the row sees; rows that are not written compute what they
     // find (a row never reaches another row's result)
@@ -515,86 +565,85 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_paged_kernel(const __grid_c
         for (int i = 0; i < 32; ++i) v[i] = 0u;
       }
     };
-    // a single: warpgroup 1 leaves its half in the ring (every product that
-    // read it is complete once both warpgroups are here), [d / 4][128] float4
+    // A single's two partial results meet in the ring (no product reads it
+    // any more once both warpgroups are here): warpgroup t finishes features
+    // t d/2 .. and leaves the others to the other, [d / 8][128] float4.
+    constexpr int kHalf = HD / 2;
     float4* sO = reinterpret_cast<float4*>(sRing);
     float2* sML = reinterpret_cast<float2*>(sRing + HD * 128 * 4);
     float w_own = 1.f, w_other = 0.f;
     if (single) {
       named_barrier_sync(1, 256);
-      if (t == 1) {
-        sML[r] = make_float2(m_ref, l_sum);
+      sML[t * 128 + r] = make_float2(m_ref, l_sum);
 #pragma unroll
-        for (int c = 0; c < HD; c += 32) {
-          uint32_t v[32];
-          read_o(c, v);
+      for (int c = 0; c < kHalf; c += 32) {
+        uint32_t v[32];
+        read_o((1 - t) * kHalf + c, v);
 #pragma unroll
-          for (int u = 0; u < 8; ++u)
-            sO[(c / 4 + u) * 128 + r] = make_float4(__uint_as_float(v[4 * u]), __uint_as_float(v[4 * u + 1]),
-                                                    __uint_as_float(v[4 * u + 2]), __uint_as_float(v[4 * u + 3]));
-        }
+        for (int u = 0; u < 8; ++u)
+          sO[(t * (kHalf / 4) + c / 4 + u) * 128 + r] =
+              make_float4(__uint_as_float(v[4 * u]), __uint_as_float(v[4 * u + 1]), __uint_as_float(v[4 * u + 2]),
+                          __uint_as_float(v[4 * u + 3]));
       }
       named_barrier_sync(1, 256);
-      if (t == 0) {
-        const float2 other = sML[r];
-        const float m = fmaxf(m_ref, other.x);
-        if (m != -INFINITY) {
-          w_own = ex2_approx(m_ref - m);
-          w_other = ex2_approx(other.x - m);
-        }
-        l_sum = l_sum * w_own + other.y * w_other;
-        m_ref = m;
+      const float2 other = sML[(1 - t) * 128 + r];
+      const float m = fmaxf(m_ref, other.x);
+      if (m != -INFINITY) {
+        w_own = ex2_approx(m_ref - m);
+        w_other = ex2_approx(other.x - m);
       }
+      l_sum = l_sum * w_own + other.y * w_other;
+      m_ref = m;
     }
-    if (!single || t == 0) {
-      const bool seen = l_sum > 0.f;
-      const bool direct = p.part_o == nullptr;
+    const bool seen = l_sum > 0.f;
+    const bool direct = p.part_o == nullptr;
+    if (direct) {
+      const float inv_l = seen ? 1.f / l_sum : 0.f;
+      w_own *= inv_l;
+      w_other *= inv_l;
+    }
+    const long long part = (static_cast<long long>(owner) * p.n_tiles + tile) * p.slots + split;
+    auto emit = [&](int c, const float* f) {  // features c .. c + 31 of the row
       if (direct) {
-        const float inv_l = seen ? 1.f / l_sum : 0.f;
-        w_own *= inv_l;
-        w_other *= inv_l;
+        T* orow = reinterpret_cast<T*>(p.o) + row.out * HD + c;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          *reinterpret_cast<uint4*>(orow + 8 * u) =
+              make_uint4(pack2<BF16>(f[8 * u], f[8 * u + 1]), pack2<BF16>(f[8 * u + 2], f[8 * u + 3]),
+                         pack2<BF16>(f[8 * u + 4], f[8 * u + 5]), pack2<BF16>(f[8 * u + 6], f[8 * u + 7]));
+      } else if (seen) {
+        // consecutive threads, consecutive float4: whole lines
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          p.part_o[(part * (HD / 4) + c / 4 + u) * 128 + r] =
+              make_float4(f[4 * u], f[4 * u + 1], f[4 * u + 2], f[4 * u + 3]);
       }
-      const long long part = (static_cast<long long>(owner) * p.n_tiles + tile) * p.slots + split;
+    };
+    const int c_lo = single ? t * kHalf : 0, c_hi = single ? c_lo + kHalf : HD;
+#pragma unroll 2
+    for (int c = c_lo; c < c_hi; c += 32) {
+      uint32_t v[32];
+      read_o(c, v);
+      float f[32];
 #pragma unroll
-      for (int c = 0; c < HD; c += 32) {
-        uint32_t v[32];
-        read_o(c, v);
-        float f[32];
+      for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]) * w_own;
+      if (single) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]) * w_own;
-        if (single) {
-#pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            const float4 y = sO[(c / 4 + u) * 128 + r];
-            f[4 * u] += y.x * w_other;
-            f[4 * u + 1] += y.y * w_other;
-            f[4 * u + 2] += y.z * w_other;
-            f[4 * u + 3] += y.w * w_other;
-          }
-        }
-        if (write) {
-          if (direct) {
-            T* orow = reinterpret_cast<T*>(p.o) + row.out * HD + c;
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-              *reinterpret_cast<uint4*>(orow + 8 * u) =
-                  make_uint4(pack2<BF16>(f[8 * u], f[8 * u + 1]), pack2<BF16>(f[8 * u + 2], f[8 * u + 3]),
-                             pack2<BF16>(f[8 * u + 4], f[8 * u + 5]), pack2<BF16>(f[8 * u + 6], f[8 * u + 7]));
-          } else if (seen) {
-            // consecutive threads, consecutive float4: whole lines
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-              p.part_o[(part * (HD / 4) + c / 4 + u) * 128 + r] =
-                  make_float4(f[4 * u], f[4 * u + 1], f[4 * u + 2], f[4 * u + 3]);
-          }
+        for (int u = 0; u < 8; ++u) {
+          const float4 y = sO[((1 - t) * (kHalf / 4) + (c - c_lo) / 4 + u) * 128 + r];
+          f[4 * u] += y.x * w_other;
+          f[4 * u + 1] += y.y * w_other;
+          f[4 * u + 2] += y.z * w_other;
+          f[4 * u + 3] += y.w * w_other;
         }
       }
-      if (write) {
-        if (direct)
-          p.lse[row.out] = seen ? (m_ref + __log2f(l_sum)) * 0.69314718055994531f : -INFINITY;
-        else
-          p.part_ml[part * 128 + r] = make_float2(seen ? m_ref : -INFINITY, l_sum);
-      }
+      if (write) emit(c, f);
+    }
+    if (write && !(single && t == 1)) {
+      if (direct)
+        p.lse[row.out] = seen ? (m_ref + __log2f(l_sum)) * 0.69314718055994531f : -INFINITY;
+      else
+        p.part_ml[part * 128 + r] = make_float2(seen ? m_ref : -INFINITY, l_sum);
     }
     tc_fence_before();
   }

@@ -4,24 +4,25 @@
 //
 // A block takes the R = G Nq <= 32 rows of one (sequence, kv head).  Each
 // cached byte is used once, for R rows, so the work is bound by memory and,
-// sequences' own parts being short, by latency: the fragments of the products
-// (16 rows x 16 keys) are loaded from the cache straight into registers, with
-// no staging and no barrier until the block's end.  The order of a product's
-// inner index is free, so the features of Q and K are dealt to the lanes in
-// 16-byte pieces: the 4 lanes of a key read 64 neighbouring bytes.  For P V the
-// lane's 4 keys are read 16 bytes at a time, the 8 lanes of a key 128
-// neighbouring bytes, and neighbouring keys paired by byte permutes.  (tcgen05
-// needs 128 keys staged in shared memory and takes its result through tensor
-// memory: the decode kernel built on it needs about 4 us for a sequence
-// of 150 keys however few they are; here a group of 16 keys is 32 small MMAs.)
+// sequences' own parts being short, by latency.  A warp therefore runs its
+// own ring of two stages (K and V rows of 16 keys at d = 128, 32 at d = 64, as
+// TMA boxes of 16 rows x 128 bytes), with no barrier between warps until
+// the end, and 16 x 16 fragments go from shared memory to mma.sync: 16 rows
+// are one of its tiles, and a group of 16 keys 32 of its instructions.
+// (tcgen05 takes 128 rows or keys at a time and its result through tensor
+// memory: the decode kernel built on it needs about 4 us for a sequence of 150
+// keys however few its rows are.)
+// The order of a product's inner index is free, so the features of Q and K
+// are dealt to the lanes in 16-byte pieces, and the pieces chosen so that the
+// 8 lanes that shared memory serves at a time meet 8 different ones of the
+// 128-byte swizzle; neighbouring keys of V are paired by byte permutes.
 //
-// Warps take groups of 16 keys in turn (with more than 16 rows, two warps per
-// group, one for each 16 rows), each with its own running max and sum; K of
-// the next group is in flight during P V of this one, V during its scores.
-// The partial results of the warps and of the prefix's splits meet at the end:
+// Each warp keeps its own running max and sum (with more than 16 rows, two
+// warps share the keys, one for each 16 rows).  The partial results of the
+// warps and of the prefix's splits meet at the end:
 //   m* = max m_s, l* = sum l_s 2^(m_s - m*), O = sum O_s 2^(m_s - m*) / l*.
-// With few sequences the own keys are split over several blocks, and
-// fa_paged_merge_kernel joins them instead.
+// With few sequences and many own keys these are split over several blocks,
+// and fa_paged_merge_kernel joins them instead.
 #pragma once
 
 #include "fa_paged.cuh"
@@ -32,11 +33,14 @@ constexpr uint32_t kKernPrefixOwn = 14;
 constexpr int kOwnWarps = 4;
 constexpr int kOwnThreads = 32 * kOwnWarps;
 
+constexpr int kOwnStages = 2;
+constexpr int kOwnStageBytes = 8192;  // K, then V: two boxes of 16 rows x 128 bytes each
+
 struct OwnParams {
   PagedParams p;        // the prefix pass: sizes, its partial results, o, lse
+  CUtensorMap tm_k;     // [num_pages * Hkv][P][d], box 64 x 16
+  CUtensorMap tm_v;
   const void* q;        // [B][Hq][N][d]
-  const void* k_cache;  // [num_pages][Hkv][P][d]
-  const void* v_cache;
   float* own_o;         // [row][S][d], [row][S][2]: with S > 1
   float* own_ml;
   int S;
@@ -55,27 +59,42 @@ __device__ __forceinline__ void mma_16816(float* c, const uint32_t* a, uint32_t 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Shared memory: the warps' O [warp][16][d] and (m, l) [warp][16].
-template <int HD>
-constexpr int own_smem() { return kOwnWarps * 16 * (HD * 4 + 8); }
+// Shared memory (from a 1024-byte boundary): the warps' rings, whose memory
+// takes their O [16][d] at the end; (m, l) of the warps' rows; the joined
+// rows' 1 / l, weights of the warps' and the prefix splits' results; barriers.
+constexpr int kOwnRing = kOwnWarps * kOwnStages * kOwnStageBytes;
+constexpr int kOwnFixed = kOwnRing + kOwnWarps * 16 * 8 + 32 * 4 + 32 * kOwnWarps * 4 + kOwnWarps * kOwnStages * 8;
+inline int own_smem(int rows, int slots) { return 1024 + kOwnFixed + rows * slots * 4; }
 
 // WM: warps that share a group of keys, one for each 16 rows.
 template <int HD, bool BF16, int WM>
-__global__ void __launch_bounds__(kOwnThreads, HD == 128 ? 2 : 4) fa_prefix_own_kernel(const __grid_constant__ OwnParams a) {
+__global__ void __launch_bounds__(kOwnThreads, 3) fa_prefix_own_kernel(const __grid_constant__ OwnParams a) {
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
   const PagedParams& p = a.p;
-  constexpr int kC = HD / 32;   // 16-byte pieces of a lane's K (or Q) row
-  constexpr int kH = HD / 64;   // 128-byte pieces of a V row
+  constexpr int kC = HD / 32;         // 16-byte pieces of a lane's K (or Q) row
+  constexpr int kH = HD / 64;         // 128-byte pieces of a row
+  constexpr int kSub = 128 / HD;      // groups of 16 keys in a stage
   constexpr int kW = kOwnWarps / WM;  // warps along the keys
-  extern __shared__ float4 own_sm[];
-  float* sO = reinterpret_cast<float*>(own_sm);
-  float2* sML = reinterpret_cast<float2*>(sO + kOwnWarps * 16 * HD);
+  extern __shared__ uint8_t own_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(own_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  float2* sML = reinterpret_cast<float2*>(sm + kOwnRing);
+  float* sInv = reinterpret_cast<float*>(sML + kOwnWarps * 16);
+  float* sWarpW = sInv + 32;                   // [row][warp along the keys]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sWarpW + 32 * kOwnWarps);
+  float* sW = reinterpret_cast<float*>(bars + kOwnWarps * kOwnStages);  // [row][slot]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nn = lane >> 2, qd = lane & 3;
   const int kw = warp / WM, mt = warp % WM;
   const int split = blockIdx.x % a.S, item = blockIdx.x / a.S;
   const int b = item / p.Hkv, g = item % p.Hkv;
   const int R = p.G * p.N;
+  uint8_t* ring = sm + warp * kOwnStages * kOwnStageBytes;
+  uint64_t* full = bars + warp * kOwnStages;
+  if (lane == 0) {
+    for (int s = 0; s < kOwnStages; ++s) mbar_init(&full[s], 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
 
   // The inputs were written before the prefix kernel started (it waits for
   // them before it lets this kernel be scheduled); only its results are
@@ -86,11 +105,47 @@ __global__ void __launch_bounds__(kOwnThreads, HD == 128 ? 2 : 4) fa_prefix_own_
   const int L = p.lens[b];
   const bool bad = L != 0 && (L < p.N || L > static_cast<long long>(p.max_pages) * p.P);
   if (bad && g == 0 && split == 0 && threadIdx.x == 0) record_error(kStatusBadInput, kKernPrefixOwn, 0, 0);
-  // groups of 16 keys: of the sequence's own part, and of this split
+  // stages of 16 kSub keys: of the sequence's own part, of this split, of this warp
+  constexpr int kKeys = 16 * kSub;
   const int own = bad || L <= p.prefix ? 0 : L - p.prefix;
-  const int n_groups = (own + 15) / 16;
-  const int g0 = static_cast<int>(static_cast<long long>(n_groups) * split / a.S);
-  const int g1 = static_cast<int>(static_cast<long long>(n_groups) * (split + 1) / a.S);
+  const int n_all = (own + kKeys - 1) / kKeys;
+  const int g0 = static_cast<int>(static_cast<long long>(n_all) * split / a.S);
+  const int g1 = static_cast<int>(static_cast<long long>(n_all) * (split + 1) / a.S);
+  const int n_mine = g1 - g0 > kw ? (g1 - g0 - kw + kW - 1) / kW : 0;
+  auto first_key = [&](int i) { return p.prefix + kKeys * (g0 + kw + i * kW); };
+  // Table entries of 16 / P-th keys: lane x holds that of group x of the
+  // warp's next 32 groups of 16 keys.
+  const int* row = p.table + static_cast<size_t>(b) * p.max_pages;
+  auto entry = [&](int grp) {
+    const int key = first_key(grp / kSub) + 16 * (grp % kSub);
+    return grp < n_mine * kSub && key < L ? __ldg(row + key / p.P) : -1;
+  };
+  int cur = entry(lane);
+  auto issue = [&](int i) {
+    if (i > 0 && i * kSub % 32 == 0) cur = entry(i * kSub + lane);
+    uint8_t* dst = ring + (i % kOwnStages) * kOwnStageBytes;
+    uint64_t* bar = &full[i % kOwnStages];
+    if (lane == 0) mbar_expect_tx(bar, kOwnStageBytes);
+    __syncwarp();
+#pragma unroll
+    for (int sub = 0; sub < kSub; ++sub) {
+      const int key = first_key(i) + 16 * sub;
+      const int phys = __shfl_sync(0xffffffffu, cur, (i * kSub + sub) & 31);
+      int outer = -1;  // outside the tensor: zeros
+      if (key < L) {
+        if (phys >= 0 && phys < p.num_pages)
+          outer = phys * p.Hkv + g;
+        else if (lane == 0)
+          record_error(kStatusBadInput, kKernPrefixOwn, 0, 1);
+      }
+      if (lane < 2 * kH) {  // lanes: K or V, chunk
+        const int c = lane % kH, is_v = lane / kH;
+        tma_load_3d(dst + is_v * (kOwnStageBytes / 2) + (kH == 2 ? c : sub) * 2048, is_v ? &a.tm_v : &a.tm_k, bar, c * 64,
+                    key % p.P, outer);
+      }
+    }
+  };
+  for (int i = 0; i < kOwnStages && i < n_mine; ++i) issue(i);
 
   // Q: rows mt * 16 + nn and + 8 as the A operand
   const T* q = static_cast<const T*>(a.q) + (static_cast<size_t>(b) * p.Hkv + g) * R * HD;
@@ -103,7 +158,7 @@ __global__ void __launch_bounds__(kOwnThreads, HD == 128 ? 2 : 4) fa_prefix_own_
 #pragma unroll
     for (int c = 0; c < kC; ++c) {
       uint4 w = make_uint4(0u, 0u, 0u, 0u);
-      if (r < R) w = *reinterpret_cast<const uint4*>(q + static_cast<size_t>(r) * HD + c * 32 + qd * 8);
+      if (r < R) w = *reinterpret_cast<const uint4*>(q + static_cast<size_t>(r) * HD + (c >> 1) * 64 + (2 * qd + (c & 1)) * 8);
       qa[c][0][e] = w.x, qa[c][0][e + 2] = w.y, qa[c][1][e] = w.z, qa[c][1][e + 2] = w.w;
     }
   }
@@ -115,66 +170,42 @@ __global__ void __launch_bounds__(kOwnThreads, HD == 128 ? 2 : 4) fa_prefix_own_
     for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
-  const int* row = p.table + static_cast<size_t>(b) * p.max_pages;
-  // element offset of key 0 of group gi in the caches, -1: nothing to load
-  auto group_base = [&](int gi) -> long long {
-    if (gi >= g1) return -1;
-    const int key = p.prefix + 16 * gi;
-    const int phys = __ldg(row + key / p.P);
-    if (phys < 0 || phys >= p.num_pages) {
-      if (lane == 0) record_error(kStatusBadInput, kKernPrefixOwn, 0, 1);
-      return -1;
-    }
-    return ((static_cast<long long>(phys) * p.Hkv + g) * p.P + key % p.P) * HD;
-  };
-  const T* kc = static_cast<const T*>(a.k_cache);
-  const T* vc = static_cast<const T*>(a.v_cache);
-  uint4 kf[2][kC], vf[4][kH];
-  // slots without a token are not read: zeros
-  auto load_k = [&](int gi, long long base) {
-    const int left = L - p.prefix - 16 * gi;  // keys from the group's first on
+  bool ok = true;
+  for (int i = 0; ok && i < n_mine; ++i) {
+    const int st = i % kOwnStages;
+    ok = __all_sync(0xffffffffu, mbar_wait_drain(&full[st], (i / kOwnStages) & 1, kKernPrefixOwn, warp, 2));
+    if (!ok) break;
+    const uint8_t* sk = ring + st * kOwnStageBytes;
+    const uint8_t* sv = sk + kOwnStageBytes / 2;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int c = 0; c < kC; ++c) {
-        kf[j][c] = make_uint4(0u, 0u, 0u, 0u);
-        if (base >= 0 && 8 * j + nn < left)
-          kf[j][c] = *reinterpret_cast<const uint4*>(kc + base + (8 * j + nn) * HD + c * 32 + qd * 8);
-      }
-  };
-  auto load_v = [&](int gi, long long base) {
-    const int left = L - p.prefix - 16 * gi;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int key = 2 * qd + (e & 1) + 8 * (e >> 1);
-#pragma unroll
-      for (int c = 0; c < kH; ++c) {
-        vf[e][c] = make_uint4(0u, 0u, 0u, 0u);
-        if (base >= 0 && key < left) vf[e][c] = *reinterpret_cast<const uint4*>(vc + base + key * HD + c * 64 + nn * 8);
-      }
-    }
-  };
-
-  int gi = g0 + kw;
-  long long base = group_base(gi), base_next = group_base(gi + kW);
-  load_k(gi, base);
-  load_v(gi, base);
-  for (; gi < g1; gi += kW) {
+    for (int sub = 0; sub < kSub; ++sub) {
+    const int key_lo = first_key(i) + 16 * sub;
+    if (key_lo >= L) break;
     float s[2][4];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
 #pragma unroll
       for (int c = 0; c < kC; ++c) {
-        mma_16816<BF16>(s[j], qa[c][0], kf[j][c].x, kf[j][c].y);
-        mma_16816<BF16>(s[j], qa[c][1], kf[j][c].z, kf[j][c].w);
+        const uint4 kf = *reinterpret_cast<const uint4*>(sk + (kH == 2 ? c >> 1 : sub) * 2048 + (8 * j + nn) * 128 +
+                                                         (((2 * qd + (c & 1)) ^ nn) << 4));
+        mma_16816<BF16>(s[j], qa[c][0], kf.x, kf.y);
+        mma_16816<BF16>(s[j], qa[c][1], kf.z, kf.w);
       }
     }
-    base = base_next;
-    base_next = group_base(gi + 2 * kW);
-    load_k(gi + kW, base);
+    uint4 vf[4][kH];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int key = 2 * qd + (e & 1) + 8 * (e >> 1);
+#pragma unroll
+      for (int c = 0; c < kH; ++c) {
+        vf[e][c] = *reinterpret_cast<const uint4*>(sv + (kH == 2 ? c : sub) * 2048 + key * 128 + ((nn ^ (key & 7)) << 4));
+        // slots without a token may hold anything: their values count as zero
+        if (key_lo + key >= L) vf[e][c] = make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
     // scores in log2 units, hidden keys -inf: element 2e + x is row e
-    const int key0 = p.prefix + 16 * gi + 2 * qd;
+    const int key0 = key_lo + 2 * qd;
     float mx[2] = {m[0], m[1]};
 #pragma unroll
     for (int j = 0; j < 2; ++j)
@@ -223,18 +254,21 @@ __global__ void __launch_bounds__(kOwnThreads, HD == 128 ? 2 : 4) fa_prefix_own_
         mma_16816<BF16>(o[8 * c + 2 * w + 1], pa, __byte_perm(v0[w], v1[w], 0x7632), __byte_perm(v2[w], v3[w], 0x7632));
       }
     }
-    load_v(gi + kW, base);
+    }
+    __syncwarp();  // every lane has read the stage
+    if (i + kOwnStages < n_mine) issue(i + kOwnStages);
   }
 
-  // The warp's rows into shared memory: lane holds features c 64 + qd 16 + i
+  // The warp's rows into its ring: lane holds features c 64 + qd 16 + i
   // (element 0 of o[8 c + i]; + 8: element 1) of rows nn (and + 8: 2, 3).
+  float* sO = reinterpret_cast<float*>(ring);
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
     l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
-    const int r = warp * 16 + nn + 8 * e;
-    if (qd == 0) sML[r] = make_float2(m[e], l[e]);
-    if (mt * 16 + nn + 8 * e < R)
+    const int r = nn + 8 * e;
+    if (qd == 0) sML[warp * 16 + r] = make_float2(m[e], l[e]);
+    if (mt * 16 + r < R)
 #pragma unroll
       for (int c = 0; c < kH; ++c)
 #pragma unroll
@@ -245,51 +279,72 @@ __global__ void __launch_bounds__(kOwnThreads, HD == 128 ? 2 : 4) fa_prefix_own_
                 make_float4(o[8 * c + i][2 * e + x], o[8 * c + i + 1][2 * e + x], o[8 * c + i + 2][2 * e + x],
                             o[8 * c + i + 3][2 * e + x]);
   }
-  if (a.S == 1 && a.follows) grid_dependency_wait();  // the prefix's partial results
-  __syncthreads();
   const bool last = a.S == 1;
+  if (last && a.follows) grid_dependency_wait();  // the prefix's partial results
+  __syncthreads();
+  // Weights of a row's partial results: a warp takes rows in turn, its lanes
+  // the prefix's splits.
   const int tile = b / p.seqs;
   const bool single = (p.n_tiles & 1) && tile == p.n_tiles - 1;
   const int slots = last ? (single ? p.S_single : p.S) : 0;  // 0 without a prefix
   const long long part = (static_cast<long long>(g) * p.n_tiles + tile) * p.slots;
+  auto tile_row = [&](int r) {  // of the prefix's tile: (sequence, token, head)
+    return ((b % p.seqs) * p.N + r % p.N) * p.G + r / p.N;
+  };
+  const long long out0 = (static_cast<long long>(b) * p.Hkv + g) * R;
+  for (int r = warp; r < R; r += kOwnWarps) {
+    const float2* ml = p.part_ml + part * 128 + tile_row(r);
+    float2 mine = make_float2(-INFINITY, 0.f);
+    if (lane < kW) mine = sML[(lane * WM + r / 16) * 16 + r % 16];
+    float ms = mine.x;
+    for (int s = lane; s < slots; s += 32) ms = fmaxf(ms, ml[s * 128].x);
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) ms = fmaxf(ms, __shfl_xor_sync(0xffffffffu, ms, x));
+    const float ref = ms == -INFINITY ? 0.f : ms;
+    float w = ex2_approx(mine.x - ref);
+    if (lane < kW) sWarpW[r * kOwnWarps + lane] = w;
+    float ls = mine.y * w;
+    for (int s = lane; s < slots; s += 32) {
+      const float2 y = ml[s * 128];
+      w = ex2_approx(y.x - ref);
+      sW[r * slots + s] = w;
+      ls += y.y * w;
+    }
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, x);
+    if (lane == 0) {
+      sInv[r] = !last ? 1.f : ls > 0.f ? 1.f / ls : 0.f;
+      if (last)
+        p.lse[out0 + r] = ls > 0.f ? (ms + __log2f(ls)) * 0.69314718055994531f : -INFINITY;
+      else
+        reinterpret_cast<float2*>(a.own_ml)[(out0 + r) * a.S + split] = make_float2(ms, ls);
+    }
+  }
+  __syncthreads();
   for (int x = threadIdx.x; x < R * (HD / 4); x += kOwnThreads) {
     const int r = x / (HD / 4), c4 = x % (HD / 4);
-    const int hg = r / p.N, t = r % p.N;
-    const int tr = ((b % p.seqs) * p.N + t) * p.G + hg;  // row of the prefix's tile: (sequence, token, head)
-    const float2* ml = p.part_ml + part * 128 + tr;
-    const float4* po = p.part_o + (part * (HD / 4) + c4) * 128 + tr;
-    float ms = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kW; ++w) ms = fmaxf(ms, sML[(w * WM + r / 16) * 16 + r % 16].x);
-#pragma unroll 8
-    for (int s = 0; s < slots; ++s) ms = fmaxf(ms, ml[s * 128].x);
-    float ls = 0.f;
+    const float4* po = p.part_o + (part * (HD / 4) + c4) * 128 + tile_row(r);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](float2 y, const float4* src) {
-      if (y.x == -INFINITY) return;
-      const float w = ex2_approx(y.x - ms);
+    auto add = [&](float w, const float4* src) {
+      if (w == 0.f) return;  // nothing there (an empty split leaves its O unwritten)
       const float4 z = *src;
-      ls += y.y * w;
       acc.x += z.x * w, acc.y += z.y * w, acc.z += z.z * w, acc.w += z.w * w;
     };
+#pragma unroll 8
+    for (int s = 0; s < slots; ++s) add(sW[r * slots + s], po + static_cast<long long>(s) * (HD / 4) * 128);
 #pragma unroll
-    for (int w = 0; w < kW; ++w) {
-      const int sr = (w * WM + r / 16) * 16 + r % 16;
-      add(sML[sr], reinterpret_cast<const float4*>(sO + sr * HD) + c4);
-    }
-#pragma unroll 4
-    for (int s = 0; s < slots; ++s) add(ml[s * 128], po + static_cast<long long>(s) * (HD / 4) * 128);
-    const long long out = (static_cast<long long>(b) * p.Hkv + g) * R + r;
+    for (int w = 0; w < kW; ++w)
+      add(sWarpW[r * kOwnWarps + w],
+          reinterpret_cast<const float4*>(sm + (w * WM + r / 16) * kOwnStages * kOwnStageBytes) + (r % 16) * (HD / 4) + c4);
+    const float inv = sInv[r];
+    acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
     if (last) {
-      const float inv = ls > 0.f ? 1.f / ls : 0.f;
       uint2 w;
-      w.x = pack2<BF16>(acc.x * inv, acc.y * inv);
-      w.y = pack2<BF16>(acc.z * inv, acc.w * inv);
-      *reinterpret_cast<uint2*>(static_cast<T*>(p.o) + out * HD + 4 * c4) = w;
-      if (c4 == 0) p.lse[out] = ls > 0.f ? (ms + __log2f(ls)) * 0.69314718055994531f : -INFINITY;
+      w.x = pack2<BF16>(acc.x, acc.y);
+      w.y = pack2<BF16>(acc.z, acc.w);
+      *reinterpret_cast<uint2*>(static_cast<T*>(p.o) + (out0 + r) * HD + 4 * c4) = w;
     } else {
-      reinterpret_cast<float4*>(a.own_o + (out * a.S + split) * HD)[c4] = acc;
-      if (c4 == 0) reinterpret_cast<float2*>(a.own_ml)[out * a.S + split] = make_float2(ms, ls);
+      reinterpret_cast<float4*>(a.own_o + ((out0 + r) * a.S + split) * HD)[c4] = acc;
     }
   }
   // the prefix kernel, too, is complete before this one is: whoever waits for
