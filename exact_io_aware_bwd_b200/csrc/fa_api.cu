@@ -930,20 +930,25 @@ fa_status_t paged_run(const PagedArgs& a, const PagedPlan& pl, void* workspace, 
       std::memset(&op, 0, sizeof(op));
       op.p = prm;
       op.S = own_splits(a.B, a.Hkv, static_cast<int64_t>(a.max_pages) * a.P - a.prefix);
+      const int64_t items = static_cast<int64_t>(a.B) * a.Hkv * op.S;
+      if (items > INT32_MAX) return FA_ERR_UNSUPPORTED;
       if (op.S > 1) {
         op.own_o = reinterpret_cast<float*>(ws + pl.bytes(d));
         op.own_ml = op.own_o + static_cast<size_t>(a.B) * a.Hq * a.N * op.S * d;
       }
       op.follows = a.prefix ? 1 : 0;
+      while ((1 << op.log2P) < a.P) ++op.log2P;
       op.q = a.q;
-      if (!make_map(&op.tm_k, a.k_cache, dt, 2, d, a.P, outer, 64, 16) ||
-          !make_map(&op.tm_v, a.v_cache, dt, 2, d, a.P, outer, 64, 16))
-        return FA_ERR_CUDA;
-      const int own_smem = fa::own_smem(G * a.N, op.S == 1 ? pl.slots() : 0);
+      op.k_cache = a.k_cache;
+      op.v_cache = a.v_cache;
+      // rings as deep as the blocks that share an SM allow
+      const int slots = op.S == 1 ? pl.slots() : 0;
+      const int per_sm = static_cast<int>(std::min<int64_t>(fa::own_blocks_per_sm(d), (items + fa::kDecodeSMs - 1) / fa::kDecodeSMs));
+      op.stages = fa::kOwnMaxStages;
+      while (op.stages > 2 && (fa::own_smem(d, op.stages, G * a.N, slots) + 1024) * per_sm > 228 * 1024) --op.stages;
+      const int own_smem = fa::own_smem(d, op.stages, G * a.N, slots);
       auto own = G * a.N > 16 ? own2 : own1;
-      if ((r = opt_in_smem(own, std::max(own_smem, fa::own_smem(32, fa::kDecodeSMs)))) != FA_OK) return r;
-      const int64_t items = static_cast<int64_t>(a.B) * a.Hkv * op.S;
-      if (items > INT32_MAX) return FA_ERR_UNSUPPORTED;
+      if ((r = opt_in_smem(own, fa::kOwnSmemLimit)) != FA_OK) return r;
       if (launch_dependent(own, dim3(static_cast<unsigned>(items)), fa::kOwnThreads, own_smem, st, op) != cudaSuccess)
         return FA_ERR_CUDA;
       if (op.S == 1) return FA_OK;

@@ -611,8 +611,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_paged_kernel(const __grid_c
           *reinterpret_cast<uint4*>(orow + 8 * u) =
               make_uint4(pack2<BF16>(f[8 * u], f[8 * u + 1]), pack2<BF16>(f[8 * u + 2], f[8 * u + 3]),
                          pack2<BF16>(f[8 * u + 4], f[8 * u + 5]), pack2<BF16>(f[8 * u + 6], f[8 * u + 7]));
-      } else if (seen) {
-        // consecutive threads, consecutive float4: whole lines
+      } else {
+        // consecutive threads, consecutive float4: whole lines (zeros where the
+        // row saw nothing: whoever joins them reads every split)
 #pragma unroll
         for (int u = 0; u < 8; ++u)
           p.part_o[(part * (HD / 4) + c / 4 + u) * 128 + r] =
@@ -698,8 +699,7 @@ __global__ void __launch_bounds__(256) fa_paged_merge_kernel(const __grid_consta
   float l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   auto add = [&](float2 x, const float4* src) {
-    if (x.x == -INFINITY) return;  // an empty split
-    const float w = ex2_approx(x.x - m);
+    const float w = ex2_approx(x.x - m);  // 0 for an empty split, whose O is 0
     const float4 y = *src;
     l += x.y * w;
     o.x += y.x * w, o.y += y.y * w, o.z += y.z * w, o.w += y.w * w;

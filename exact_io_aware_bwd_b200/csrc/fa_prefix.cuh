@@ -5,17 +5,20 @@
 // A block takes the R = G Nq <= 32 rows of one (sequence, kv head).  Each
 // cached byte is used once, for R rows, so the work is bound by memory and,
 // sequences' own parts being short, by latency.  A warp therefore runs its
-// own ring of two stages (K and V rows of 16 keys at d = 128, 32 at d = 64, as
-// TMA boxes of 16 rows x 128 bytes), with no barrier between warps until
-// the end, and 16 x 16 fragments go from shared memory to mma.sync: 16 rows
-// are one of its tiles, and a group of 16 keys 32 of its instructions.
+// own ring of stages (K and V rows of 16 keys; as many stages as the blocks on
+// an SM leave room for), with no barrier between warps until the end, and
+// 16 x 16 fragments go from shared memory to mma.sync: 16 rows are one of its
+// tiles, and a stage 32 of its instructions at d = 128.  The stages are filled
+// by 16-byte asynchronous copies of all lanes: as TMA boxes of 16 rows x 128
+// bytes, at some 40 ns a box on an SM, they alone took 0.5 us a stage.
 // (tcgen05 takes 128 rows or keys at a time and its result through tensor
 // memory: the decode kernel built on it needs about 4 us for a sequence of 150
 // keys however few its rows are.)
-// The order of a product's inner index is free, so the features of Q and K
-// are dealt to the lanes in 16-byte pieces, and the pieces chosen so that the
-// 8 lanes that shared memory serves at a time meet 8 different ones of the
-// 128-byte swizzle; neighbouring keys of V are paired by byte permutes.
+// A warp's time is its instructions (two or three warps share a scheduler), so
+// a stage is kept to about 150 of them: fragments by ldmatrix from 128-byte
+// swizzled rows, a reference max that moves only when a score exceeds it by
+// more than 8 (log2), the mask, the clearing of rows without a token and the
+// table look-up outside the common path.
 //
 // Each warp keeps its own running max and sum (with more than 16 rows, two
 // warps share the keys, one for each 16 rows).  The partial results of the
@@ -33,19 +36,33 @@ constexpr uint32_t kKernPrefixOwn = 14;
 constexpr int kOwnWarps = 4;
 constexpr int kOwnThreads = 32 * kOwnWarps;
 
-constexpr int kOwnStages = 2;
-constexpr int kOwnStageBytes = 8192;  // K, then V: two boxes of 16 rows x 128 bytes each
+constexpr int kOwnMaxStages = 8;
+// a stage: K, then V rows of 16 keys
+__host__ __device__ constexpr int own_stage_bytes(int d) { return 2 * 16 * d * 2; }
+// blocks that an SM's registers hold
+__host__ __device__ constexpr int own_blocks_per_sm(int d) { return d == 128 ? 3 : 4; }
 
 struct OwnParams {
   PagedParams p;        // the prefix pass: sizes, its partial results, o, lse
-  CUtensorMap tm_k;     // [num_pages * Hkv][P][d], box 64 x 16
-  CUtensorMap tm_v;
   const void* q;        // [B][Hq][N][d]
+  const void* k_cache;  // [num_pages][Hkv][P][d]
+  const void* v_cache;
   float* own_o;         // [row][S][d], [row][S][2]: with S > 1
   float* own_ml;
   int S;
+  int stages;           // of a warp's ring
+  int log2P;            // log2 of the page size
   int follows;          // the prefix kernel precedes this one in the stream
 };
+
+// 16 bytes global -> shared, the bytes behind the first `bytes` as zeros.
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+// Arrives on `bar` once this thread's copies so far have landed.
+__device__ __forceinline__ void copies_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
 
 template <bool BF16>
 __device__ __forceinline__ void mma_16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -61,37 +78,55 @@ __device__ __forceinline__ void mma_16816(float* c, const uint32_t* a, uint32_t 
 
 // Shared memory (from a 1024-byte boundary): the warps' rings, whose memory
 // takes their O [16][d] at the end; (m, l) of the warps' rows; the joined
-// rows' 1 / l, weights of the warps' and the prefix splits' results; barriers.
-constexpr int kOwnRing = kOwnWarps * kOwnStages * kOwnStageBytes;
-constexpr int kOwnFixed = kOwnRing + kOwnWarps * 16 * 8 + 32 * 4 + 32 * kOwnWarps * 4 + kOwnWarps * kOwnStages * 8;
-inline int own_smem(int rows, int slots) { return 1024 + kOwnFixed + rows * slots * 4; }
+// rows' 1 / l, weights of the warps' results; barriers; weights of the prefix
+// splits' results.
+constexpr int kOwnFixed = kOwnWarps * 16 * 8 + 32 * 4 + 32 * kOwnWarps * 4 + kOwnWarps * kOwnMaxStages * 8;
+inline int own_smem(int d, int stages, int rows, int slots) {
+  return 1024 + kOwnWarps * stages * own_stage_bytes(d) + kOwnFixed + rows * slots * 4;
+}
+
+constexpr int kOwnSmemLimit = 227 * 1024;
+
+__device__ __forceinline__ void ldmatrix_x4(uint32_t* r, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t* r, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
 
 // WM: warps that share a group of keys, one for each 16 rows.
 template <int HD, bool BF16, int WM>
-__global__ void __launch_bounds__(kOwnThreads, 3) fa_prefix_own_kernel(const __grid_constant__ OwnParams a) {
+__global__ void __launch_bounds__(kOwnThreads, own_blocks_per_sm(HD)) fa_prefix_own_kernel(const __grid_constant__ OwnParams a) {
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
   const PagedParams& p = a.p;
-  constexpr int kC = HD / 32;         // 16-byte pieces of a lane's K (or Q) row
-  constexpr int kH = HD / 64;         // 128-byte pieces of a row
-  constexpr int kSub = 128 / HD;      // groups of 16 keys in a stage
+  constexpr int kStage = own_stage_bytes(HD);
+  constexpr int kSteps = HD / 16;     // inner steps of a score
   constexpr int kW = kOwnWarps / WM;  // warps along the keys
+  constexpr float kSlack = 8.f;
   extern __shared__ uint8_t own_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(own_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  float2* sML = reinterpret_cast<float2*>(sm + kOwnRing);
+  const int NS = a.stages;
+  float2* sML = reinterpret_cast<float2*>(sm + kOwnWarps * NS * kStage);
   float* sInv = reinterpret_cast<float*>(sML + kOwnWarps * 16);
   float* sWarpW = sInv + 32;                   // [row][warp along the keys]
   uint64_t* bars = reinterpret_cast<uint64_t*>(sWarpW + 32 * kOwnWarps);
-  float* sW = reinterpret_cast<float*>(bars + kOwnWarps * kOwnStages);  // [row][slot]
+  float* sW = reinterpret_cast<float*>(bars + kOwnWarps * kOwnMaxStages);  // [row][slot]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nn = lane >> 2, qd = lane & 3;
   const int kw = warp / WM, mt = warp % WM;
   const int split = blockIdx.x % a.S, item = blockIdx.x / a.S;
   const int b = item / p.Hkv, g = item % p.Hkv;
   const int R = p.G * p.N;
-  uint8_t* ring = sm + warp * kOwnStages * kOwnStageBytes;
-  uint64_t* full = bars + warp * kOwnStages;
+  const uint32_t ring = smem_u32(sm) + warp * NS * kStage;
+  uint64_t* full = bars + warp * kOwnMaxStages;
   if (lane == 0) {
-    for (int s = 0; s < kOwnStages; ++s) mbar_init(&full[s], 1);
+    for (int s = 0; s < NS; ++s) mbar_init(&full[s], 32);
     fence_mbar_init();
   }
   __syncwarp();
@@ -105,132 +140,152 @@ __global__ void __launch_bounds__(kOwnThreads, 3) fa_prefix_own_kernel(const __g
   const int L = p.lens[b];
   const bool bad = L != 0 && (L < p.N || L > static_cast<long long>(p.max_pages) * p.P);
   if (bad && g == 0 && split == 0 && threadIdx.x == 0) record_error(kStatusBadInput, kKernPrefixOwn, 0, 0);
-  // stages of 16 kSub keys: of the sequence's own part, of this split, of this warp
-  constexpr int kKeys = 16 * kSub;
+  // groups of 16 keys: of the sequence's own part, of this split, of this warp
   const int own = bad || L <= p.prefix ? 0 : L - p.prefix;
-  const int n_all = (own + kKeys - 1) / kKeys;
-  const int g0 = static_cast<int>(static_cast<long long>(n_all) * split / a.S);
-  const int g1 = static_cast<int>(static_cast<long long>(n_all) * (split + 1) / a.S);
+  const int n_all = (own + 15) / 16;
+  const int g0 = a.S == 1 ? 0 : static_cast<int>(static_cast<long long>(n_all) * split / a.S);
+  const int g1 = a.S == 1 ? n_all : static_cast<int>(static_cast<long long>(n_all) * (split + 1) / a.S);
   const int n_mine = g1 - g0 > kw ? (g1 - g0 - kw + kW - 1) / kW : 0;
-  auto first_key = [&](int i) { return p.prefix + kKeys * (g0 + kw + i * kW); };
-  // Table entries of 16 / P-th keys: lane x holds that of group x of the
-  // warp's next 32 groups of 16 keys.
+  auto first_key = [&](int i) { return p.prefix + 16 * (g0 + kw + i * kW); };
+  // Table entries of the warp's groups, 32 at a time, one a lane (unsplit, the
+  // first ones are asked for before the length is known).
   const int* row = p.table + static_cast<size_t>(b) * p.max_pages;
-  auto entry = [&](int grp) {
-    const int key = first_key(grp / kSub) + 16 * (grp % kSub);
-    return grp < n_mine * kSub && key < L ? __ldg(row + key / p.P) : -1;
+  auto entry = [&](int i) {
+    const int page = first_key(i) >> a.log2P;
+    return page < p.max_pages ? __ldg(row + page) : -1;
   };
   int cur = entry(lane);
-  auto issue = [&](int i) {
-    if (i > 0 && i * kSub % 32 == 0) cur = entry(i * kSub + lane);
-    uint8_t* dst = ring + (i % kOwnStages) * kOwnStageBytes;
-    uint64_t* bar = &full[i % kOwnStages];
-    if (lane == 0) mbar_expect_tx(bar, kOwnStageBytes);
-    __syncwarp();
+
+  // A stage: 16 rows of K, then of V, contiguous in the cache; in shared
+  // memory chunks of 64 features [16][128 bytes], 16-byte pieces swizzled by
+  // row.  Lane: 16 bytes of every 512.
+  constexpr int kRowLanes = HD / 8, kRows = 32 / kRowLanes;  // lanes of a row, rows of a copy
+  const int lr = lane / kRowLanes;
+  uint32_t to[8 / kRows];  // where the lane's piece goes, for rows lr, lr + kRows, .. below 8
 #pragma unroll
-    for (int sub = 0; sub < kSub; ++sub) {
-      const int key = first_key(i) + 16 * sub;
-      const int phys = __shfl_sync(0xffffffffu, cur, (i * kSub + sub) & 31);
-      int outer = -1;  // outside the tensor: zeros
-      if (key < L) {
-        if (phys >= 0 && phys < p.num_pages)
-          outer = phys * p.Hkv + g;
-        else if (lane == 0)
-          record_error(kStatusBadInput, kKernPrefixOwn, 0, 1);
+  for (int x = 0; x < 8 / kRows; ++x) {
+    const int piece = lane % kRowLanes, r = x * kRows + lr;
+    to[x] = (piece >> 3) * 2048 + r * 128 + (((piece & 7) ^ r) << 4);
+  }
+  const T* kc = static_cast<const T*>(a.k_cache) + lane * 8;
+  const T* vc = static_cast<const T*>(a.v_cache) + lane * 8;
+  const uint32_t ring_end = ring + NS * kStage;
+  uint32_t dst = ring;  // stage of the next group to load
+  uint64_t* dst_bar = full;
+  auto issue = [&](int i) {
+    if (i > 0 && i % 32 == 0) cur = entry(i + lane);
+    const int key = first_key(i);
+    const int phys = __shfl_sync(0xffffffffu, cur, i & 31);
+    const bool page_ok = phys >= 0 && phys < p.num_pages;
+    if (page_ok && key + 16 <= L) {
+      const long long src = ((static_cast<long long>(phys) * p.Hkv + g) * p.P + (key & (p.P - 1))) * HD;
+#pragma unroll
+      for (int x = 0; x < 16 / kRows; ++x) {
+        const uint32_t t = dst + to[x % (8 / kRows)] + x / (8 / kRows) * 1024;
+        copy16_async(t, kc + src + x * 256, 16);
+        copy16_async(t + kStage / 2, vc + src + x * 256, 16);
       }
-      if (lane < 2 * kH) {  // lanes: K or V, chunk
-        const int c = lane % kH, is_v = lane / kH;
-        tma_load_3d(dst + is_v * (kOwnStageBytes / 2) + (kH == 2 ? c : sub) * 2048, is_v ? &a.tm_v : &a.tm_k, bar, c * 64,
-                    key % p.P, outer);
+    } else {
+      // rows without a token, which may hold anything, become zeros
+      if (!page_ok && lane == 0) record_error(kStatusBadInput, kKernPrefixOwn, 0, 1);
+      const long long src = page_ok ? ((static_cast<long long>(phys) * p.Hkv + g) * p.P + (key & (p.P - 1))) * HD : 0;
+#pragma unroll 1
+      for (int x = 0; x < 16 / kRows; ++x) {
+        const int r = x * kRows + lr, piece = lane % kRowLanes;
+        const uint32_t t = dst + (piece >> 3) * 2048 + r * 128 + (((piece & 7) ^ (r & 7)) << 4);
+        const int bytes = page_ok && key + r < L ? 16 : 0;
+        copy16_async(t, kc + src + x * 256, bytes);
+        copy16_async(t + kStage / 2, vc + src + x * 256, bytes);
       }
     }
+    copies_arrive(dst_bar);
+    dst += kStage, ++dst_bar;
+    if (dst == ring_end) dst = ring, dst_bar = full;
   };
-  for (int i = 0; i < kOwnStages && i < n_mine; ++i) issue(i);
+  for (int i = 0; i < NS && i < n_mine; ++i) issue(i);
 
   // Q: rows mt * 16 + nn and + 8 as the A operand
   const T* q = static_cast<const T*>(a.q) + (static_cast<size_t>(b) * p.Hkv + g) * R * HD;
-  uint32_t qa[kC][2][4];
+  uint32_t qa[kSteps][4];
   int lim[2];  // last key the two rows see
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     const int r = mt * 16 + nn + 8 * e;
     lim[e] = L - p.N + r % p.N;
 #pragma unroll
-    for (int c = 0; c < kC; ++c) {
-      uint4 w = make_uint4(0u, 0u, 0u, 0u);
-      if (r < R) w = *reinterpret_cast<const uint4*>(q + static_cast<size_t>(r) * HD + (c >> 1) * 64 + (2 * qd + (c & 1)) * 8);
-      qa[c][0][e] = w.x, qa[c][0][e + 2] = w.y, qa[c][1][e] = w.z, qa[c][1][e + 2] = w.w;
+    for (int k = 0; k < kSteps; ++k) {
+      qa[k][e] = qa[k][e + 2] = 0u;
+      if (r < R) {
+        const uint32_t* src = reinterpret_cast<const uint32_t*>(q + static_cast<size_t>(r) * HD + k * 16 + 2 * qd);
+        qa[k][e] = src[0];
+        qa[k][e + 2] = src[4];
+      }
     }
   }
 
-  float o[8 * kH][4];
+  float o[HD / 8][4];  // features 8 j + 2 qd, + 1 of rows nn (0, 1) and nn + 8 (2, 3)
 #pragma unroll
-  for (int j = 0; j < 8 * kH; ++j)
+  for (int j = 0; j < HD / 8; ++j)
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  const float c_log2 = p.scale_log2;
 
-  bool ok = true;
-  for (int i = 0; ok && i < n_mine; ++i) {
-    const int st = i % kOwnStages;
-    ok = __all_sync(0xffffffffu, mbar_wait_drain(&full[st], (i / kOwnStages) & 1, kKernPrefixOwn, warp, 2));
-    if (!ok) break;
-    const uint8_t* sk = ring + st * kOwnStageBytes;
-    const uint8_t* sv = sk + kOwnStageBytes / 2;
-#pragma unroll
-    for (int sub = 0; sub < kSub; ++sub) {
-    const int key_lo = first_key(i) + 16 * sub;
-    if (key_lo >= L) break;
-    float s[2][4];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
-#pragma unroll
-      for (int c = 0; c < kC; ++c) {
-        const uint4 kf = *reinterpret_cast<const uint4*>(sk + (kH == 2 ? c >> 1 : sub) * 2048 + (8 * j + nn) * 128 +
-                                                         (((2 * qd + (c & 1)) ^ nn) << 4));
-        mma_16816<BF16>(s[j], qa[c][0], kf.x, kf.y);
-        mma_16816<BF16>(s[j], qa[c][1], kf.z, kf.w);
-      }
-    }
-    uint4 vf[4][kH];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int key = 2 * qd + (e & 1) + 8 * (e >> 1);
-#pragma unroll
-      for (int c = 0; c < kH; ++c) {
-        vf[e][c] = *reinterpret_cast<const uint4*>(sv + (kH == 2 ? c : sub) * 2048 + key * 128 + ((nn ^ (key & 7)) << 4));
-        // slots without a token may hold anything: their values count as zero
-        if (key_lo + key >= L) vf[e][c] = make_uint4(0u, 0u, 0u, 0u);
-      }
-    }
-    // scores in log2 units, hidden keys -inf: element 2e + x is row e
-    const int key0 = key_lo + 2 * qd;
-    float mx[2] = {m[0], m[1]};
+  // the lane's row addresses for ldmatrix: K keys l & 7 (+ 8: lanes 16 up),
+  // pieces 0, 1; V keys l & 15, pieces 0, 1
+  const int k_key = (lane & 7) + 8 * (lane >> 4), v_key = lane & 15;
+  const uint32_t k_off = k_key * 128 + ((((lane >> 3) & 1) ^ (k_key & 7)) << 4);
+  const uint32_t v_off = v_key * 128 + (((lane >> 4) ^ (v_key & 7)) << 4) + kStage / 2;
+
+  uint32_t st = ring;  // stage of group i
+  uint64_t* st_bar = full;
+  uint32_t phase = 0;
+  for (int i = 0; i < n_mine; ++i) {
+    if (!__all_sync(0xffffffffu, mbar_wait_drain(st_bar, phase, kKernPrefixOwn, warp, 2))) break;
+    float s[2][4], s2[2][4];  // two sums: four chains of MMAs side by side
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float v = s[j][e] * p.scale_log2;
-        s[j][e] = key0 + 8 * j + (e & 1) <= lim[e >> 1] ? v : -INFINITY;
-        mx[e >> 1] = fmaxf(mx[e >> 1], s[j][e]);
-      }
-    float fac[2];
+      for (int e = 0; e < 4; ++e) s[j][e] = s2[j][e] = 0.f;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
-      mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
-      fac[e] = mx[e] == -INFINITY ? 1.f : ex2_approx(m[e] - mx[e]);
+    for (int k = 0; k < kSteps; ++k) {
+      uint32_t kf[4];
+      ldmatrix_x4(kf, (st + k_off + (k >> 2) * 2048) ^ ((k & 3) << 5));
+      mma_16816<BF16>(k & 1 ? s2[0] : s[0], qa[k], kf[0], kf[1]);
+      mma_16816<BF16>(k & 1 ? s2[1] : s[1], qa[k], kf[2], kf[3]);
     }
-    const bool moves = mx[0] > m[0] || mx[1] > m[1];
-    if (__any_sync(0xffffffffu, moves)) {
 #pragma unroll
-      for (int j = 0; j < 8 * kH; ++j) {
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[j][e] += s2[j][e];
+    const int key_lo = first_key(i);
+    if (key_lo + 15 > L - p.N) {  // keys that some row does not see
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (key_lo + 8 * j + 2 * qd + (e & 1) > lim[e >> 1]) s[j][e] = -INFINITY;
+    }
+    float mx[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      mx[e] = fmaxf(fmaxf(s[0][2 * e], s[0][2 * e + 1]), fmaxf(s[1][2 * e], s[1][2 * e + 1])) * c_log2;
+    if (__any_sync(0xffffffffu, mx[0] > m[0] + kSlack || mx[1] > m[1] + kSlack)) {
+      float fac[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
+        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
+        mx[e] = fmaxf(mx[e], m[e]);
+        fac[e] = mx[e] == -INFINITY ? 1.f : ex2_approx(m[e] - mx[e]);
+        l[e] *= fac[e];
+        m[e] = mx[e];
+      }
+#pragma unroll
+      for (int j = 0; j < HD / 8; ++j) {
         o[j][0] *= fac[0], o[j][1] *= fac[0];
         o[j][2] *= fac[1], o[j][3] *= fac[1];
       }
-      l[0] *= fac[0], l[1] *= fac[1];
-      m[0] = mx[0], m[1] = mx[1];
     }
     const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
     uint32_t pa[4];
@@ -238,30 +293,25 @@ __global__ void __launch_bounds__(kOwnThreads, 3) fa_prefix_own_kernel(const __g
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float x = ex2_approx(s[j][2 * e] - ref[e]), y = ex2_approx(s[j][2 * e + 1] - ref[e]);
+        const float x = ex2_approx(fmaf(s[j][2 * e], c_log2, -ref[e])), y = ex2_approx(fmaf(s[j][2 * e + 1], c_log2, -ref[e]));
         l[e] += x + y;
         pa[2 * j + e] = pack2<BF16>(x, y);
       }
 #pragma unroll
-    for (int c = 0; c < kH; ++c) {
-      const uint32_t* v0 = reinterpret_cast<const uint32_t*>(&vf[0][c]);
-      const uint32_t* v1 = reinterpret_cast<const uint32_t*>(&vf[1][c]);
-      const uint32_t* v2 = reinterpret_cast<const uint32_t*>(&vf[2][c]);
-      const uint32_t* v3 = reinterpret_cast<const uint32_t*>(&vf[3][c]);
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        mma_16816<BF16>(o[8 * c + 2 * w], pa, __byte_perm(v0[w], v1[w], 0x5410), __byte_perm(v2[w], v3[w], 0x5410));
-        mma_16816<BF16>(o[8 * c + 2 * w + 1], pa, __byte_perm(v0[w], v1[w], 0x7632), __byte_perm(v2[w], v3[w], 0x7632));
-      }
-    }
+    for (int j = 0; j < HD / 8; j += 2) {
+      uint32_t vf[4];
+      ldmatrix_x4_trans(vf, (st + v_off + (j >> 3) * 2048) ^ ((j & 7) << 4));
+      mma_16816<BF16>(o[j], pa, vf[0], vf[1]);
+      mma_16816<BF16>(o[j + 1], pa, vf[2], vf[3]);
     }
     __syncwarp();  // every lane has read the stage
-    if (i + kOwnStages < n_mine) issue(i + kOwnStages);
+    if (i + NS < n_mine) issue(i + NS);
+    st += kStage, ++st_bar;
+    if (st == ring_end) st = ring, st_bar = full, phase ^= 1;
   }
 
-  // The warp's rows into its ring: lane holds features c 64 + qd 16 + i
-  // (element 0 of o[8 c + i]; + 8: element 1) of rows nn (and + 8: 2, 3).
-  float* sO = reinterpret_cast<float*>(ring);
+  // The warp's rows into its ring.
+  float* sO = reinterpret_cast<float*>(sm + warp * NS * kStage);
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
@@ -270,14 +320,8 @@ __global__ void __launch_bounds__(kOwnThreads, 3) fa_prefix_own_kernel(const __g
     if (qd == 0) sML[warp * 16 + r] = make_float2(m[e], l[e]);
     if (mt * 16 + r < R)
 #pragma unroll
-      for (int c = 0; c < kH; ++c)
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-          for (int i = 0; i < 8; i += 4)
-            *reinterpret_cast<float4*>(sO + r * HD + c * 64 + qd * 16 + 8 * x + i) =
-                make_float4(o[8 * c + i][2 * e + x], o[8 * c + i + 1][2 * e + x], o[8 * c + i + 2][2 * e + x],
-                            o[8 * c + i + 3][2 * e + x]);
+      for (int j = 0; j < HD / 8; ++j)
+        *reinterpret_cast<float2*>(sO + r * HD + 8 * j + 2 * qd) = make_float2(o[j][2 * e], o[j][2 * e + 1]);
   }
   const bool last = a.S == 1;
   if (last && a.follows) grid_dependency_wait();  // the prefix's partial results
@@ -322,11 +366,10 @@ __global__ void __launch_bounds__(kOwnThreads, 3) fa_prefix_own_kernel(const __g
   }
   __syncthreads();
   for (int x = threadIdx.x; x < R * (HD / 4); x += kOwnThreads) {
-    const int r = x / (HD / 4), c4 = x % (HD / 4);
+    const int r = x % R, c4 = x / R;  // rows fastest: neighbours in the prefix's partial results
     const float4* po = p.part_o + (part * (HD / 4) + c4) * 128 + tile_row(r);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     auto add = [&](float w, const float4* src) {
-      if (w == 0.f) return;  // nothing there (an empty split leaves its O unwritten)
       const float4 z = *src;
       acc.x += z.x * w, acc.y += z.y * w, acc.z += z.z * w, acc.w += z.w * w;
     };
@@ -335,7 +378,7 @@ __global__ void __launch_bounds__(kOwnThreads, 3) fa_prefix_own_kernel(const __g
 #pragma unroll
     for (int w = 0; w < kW; ++w)
       add(sWarpW[r * kOwnWarps + w],
-          reinterpret_cast<const float4*>(sm + (w * WM + r / 16) * kOwnStages * kOwnStageBytes) + (r % 16) * (HD / 4) + c4);
+          reinterpret_cast<const float4*>(sm + (w * WM + r / 16) * NS * kStage) + (r % 16) * (HD / 4) + c4);
     const float inv = sInv[r];
     acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
     if (last) {
