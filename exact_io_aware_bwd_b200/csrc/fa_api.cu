@@ -792,8 +792,8 @@ struct PagedPlan {
 };
 
 // Splits by a model of the time, in steps of one row tile on one key tile
-// (0.62 us at d = 128, half of a pair's): a block costs its steps and 6 more
-// for its start and end; blocks run in waves of one per SM; joining costs 5
+// (1 us, half of a pair's): a block costs its steps and 5 more for its start
+// and end; blocks run in waves of one per SM; joining costs 5
 // steps for the launch and the partial results' way through L2 (a row of a
 // split: 8 d + 16 bytes at 5 TB/s).  Up to a wave of splits, at least 2 key
 // tiles each.
@@ -819,8 +819,8 @@ PagedPlan paged_plan(int B, int Hq, int Hkv, int N, int d, int64_t keys, bool pr
     const int64_t blocks = pl.owners * (pairs * S + odd * Ss);
     const double waves = static_cast<double>(blocks) / fa::kDecodeSMs;
     const double steps = std::max(pairs ? 2.0 * ((tiles + S - 1) / S) : 0.0, odd ? 1.0 * ((tiles + Ss - 1) / Ss) : 0.0);
-    double cost = (waves <= 4 ? std::ceil(waves) : waves) * (steps + 6);
-    if (S > 1 || prefix) cost += 5 + static_cast<double>(pl.rows()) * S * (8.0 * d + 16) / 5e12 / 0.62e-6;
+    double cost = (waves <= 4 ? std::ceil(waves) : waves) * (steps + 5);
+    if (S > 1 || prefix) cost += 5 + static_cast<double>(pl.rows()) * S * (8.0 * d + 16) / 5e12 / 1e-6;
     if (cost < best) {
       best = cost;
       pl.S = static_cast<int>(S);
@@ -965,7 +965,7 @@ fa_status_t paged_run(const PagedArgs& a, const PagedPlan& pl, void* workspace, 
   };
 #define FA_PAGED_RUN(HD, BFV) \
   run(fa::fa_paged_kernel<HD, BFV>, fa::fa_prefix_own_kernel<HD, BFV, 1>, fa::fa_prefix_own_kernel<HD, BFV, 2>, \
-      fa::fa_paged_merge_kernel<HD, BFV>, fa::FwdLayout<HD>::kDynSmem)
+      fa::fa_paged_merge_kernel<HD, BFV>, fa::PagedLayout<HD>::kBytes)
   if (d == 128) return bf ? FA_PAGED_RUN(128, true) : FA_PAGED_RUN(128, false);
   return bf ? FA_PAGED_RUN(64, true) : FA_PAGED_RUN(64, false);
 #undef FA_PAGED_RUN
@@ -1032,15 +1032,18 @@ fa_status_t fa_append_paged(const void* q, const void* k, const void* v, const i
   prm.tok_per_block = tpb;
   const int64_t gx = (prm.tokens + tpb - 1) / tpb;
   if (gx > INT32_MAX) return FA_ERR_UNSUPPORTED;
-  // the heads in gy parts: enough blocks for 4 per SM, but no thread with
-  // fewer than kAppendHeads heads while there is a block for each SM
+  // The heads in gy parts: enough blocks for kBlocks per SM as long as threads
+  // keep whole rounds of kAppendHeads heads, and for one per SM as long as
+  // they keep a head.
+  constexpr int64_t kBlocks = 24;
   const int heads = (q ? Hq : 0) + 2 * Hkv, lanes = rows / tpb;
   const int sms = sm_count();
   if (sms <= 0) return FA_ERR_CUDA;
-  const int64_t most = (heads + lanes - 1) / lanes;                                       // one head a thread
-  const int64_t full = std::max<int64_t>(1, most / fa::kAppendHeads);                     // kAppendHeads each
-  const int64_t want = (4ll * sms + gx - 1) / gx, least = (sms + gx - 1) / gx;
-  const int64_t gy = std::min<int64_t>(std::max(std::min(want, full), std::min(least, most)), 65535);
+  const int64_t most = (heads + lanes - 1) / lanes;  // heads of a thread with gy = 1
+  auto parts = [&](int64_t per_sm) { return (per_sm * sms + gx - 1) / gx; };
+  const int64_t rounds = std::max<int64_t>(1, most / (fa::kAppendHeads * parts(kBlocks)));
+  const int64_t whole = std::max<int64_t>(1, most / (fa::kAppendHeads * rounds));
+  const int64_t gy = std::min<int64_t>(std::max(std::min(whole, parts(kBlocks)), std::min(most, parts(1))), 65535);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool bf = dtype == FA_BF16;
   auto kern = bf ? (interleaved ? fa::fa_append_kernel<true, true> : fa::fa_append_kernel<true, false>)

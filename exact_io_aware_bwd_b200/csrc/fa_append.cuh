@@ -54,7 +54,7 @@ struct AppendParams {
 constexpr double kInvTwoPi = 0.15915494309189533576888;
 
 template <bool BF16, bool INTER>
-__global__ void __launch_bounds__(kAppendThreads) fa_append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, 3) fa_append_kernel(const __grid_constant__ AppendParams p) {
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
   using T2 = typename std::conditional<BF16, __nv_bfloat162, __half2>::type;
   grid_dependency_wait();

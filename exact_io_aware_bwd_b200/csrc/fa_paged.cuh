@@ -113,7 +113,7 @@ __device__ __forceinline__ PagedRow paged_row(const PagedParams& p, int owner, i
   return w;
 }
 
-// One block's work.
+// A block's work: a pair of row tiles or a single, and a range of key tiles.
 struct PagedItem {
   bool single;  // one row tile, its key tiles shared out between the warpgroups
   bool dead;    // only padding rows: nothing is written
@@ -122,13 +122,13 @@ struct PagedItem {
   int k0, n_kv;   // key tiles
 };
 
-// Pairs first, the last tokens (most keys) of every sequence first; then the
-// singles, which take half a pair's time.
+// Blocks in order: pairs first, the last tokens (most keys) of every sequence
+// first; then the singles, which take half a pair's time.
 __device__ __forceinline__ PagedItem paged_item(const PagedParams& p) {
   PagedItem it;
+  int x = blockIdx.x;
   const int owners = p.decode ? p.Hkv : p.B * p.Hkv;
   const int n_pairs = p.n_tiles / 2;
-  int x = blockIdx.x;
   it.single = x >= n_pairs * owners * p.S;
   if (it.single) x -= n_pairs * owners * p.S;
   const int splits = it.single ? p.S_single : p.S;
@@ -169,14 +169,24 @@ __device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
+// Shared memory: the forward kernel's layout and, behind it, (m, l) of both
+// warpgroups' rows.  Nothing is left at d = 128 to re-align the base with; the
+// dynamic shared memory of a block without static shared memory starts on a
+// 1024-byte boundary (checked).
+template <int HD>
+struct PagedLayout : FwdLayout<HD> {
+  static constexpr int kOffML = (FwdLayout<HD>::kSmemBytes + 15) / 16 * 16;
+  static constexpr int kBytes = kOffML + 2 * 128 * 8;
+  static_assert(kBytes <= 232448, "shared memory budget");
+};
+
 template <int HD, bool BF16>
 __global__ void __launch_bounds__(kFwdThreads, 1) fa_paged_kernel(const __grid_constant__ PagedParams p) {
-  using L = FwdLayout<HD>;
+  using L = PagedLayout<HD>;
   using T = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
   constexpr int NS = L::kSlots;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                           ~static_cast<uintptr_t>(1023));
+  uint8_t* sm = smem_raw;
   uint8_t* sQ = sm + L::kOffQ;
   uint8_t* sRing = sm + L::kOffRing;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::kOffBar);
@@ -187,55 +197,21 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_paged_kernel(const __grid_c
   uint64_t* p_half = s_full + 2;  // [warpgroup][half]
   uint64_t* pv_done = p_half + 4;
   uint64_t* done_bar = pv_done + 2;
+  float2* sML = reinterpret_cast<float2*>(sm + L::kOffML);
   uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(sm + L::kOffTmemPtr);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::kOffAbort);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (smem_u32(sm) & 1023u) {  // refuse
+    if (tid == 0) record_error(kStatusSmemAlign, kKernPaged, 0, 0);
+    return;
+  }
   const int box_rows = p.G * p.toks * p.seqs;  // rows of a tile that the q box fills
 
   // The third warpgroup gives its registers up at once, so that the softmax
   // warpgroups need not wait for them behind the first loads.
   if (warp >= 8) setmaxnreg_dec<kFwdOtherRegs>();
-  // ------------------------------------------------------------ producers
-  // Warp 9 loads K tiles (and q), warp 10 V tiles, the first ones before the
-  // block's other warps are set up.
   const bool produces = warp == 9 || warp == 10;
-  const int which = warp - 9;
-  const int ppt = kPagedTile / p.P;  // pages of a key tile
-  PagedItem it = {};
-  int cur = -1, nxt = -1;  // table entries of 32 pages, one a lane, and of the next 32
-  auto entry = [&](int rel) {  // of the page `rel` after the item's first
-    const int pg = it.k0 * ppt + rel;
-    return pg < (it.valid_end + p.P - 1) / p.P ? __ldg(p.table + static_cast<size_t>(it.b) * p.max_pages + pg) : -1;
-  };
-  auto load_tile = [&](int kt) -> bool {
-    const int rel = kt * ppt;
-    if (kt > 0 && rel % 32 == 0) {
-      cur = nxt;
-      nxt = entry(rel + 32 + lane);
-    }
-    const int phys = __shfl_sync(0xffffffffu, cur, (rel + lane) & 31);
-    int outer = -1;  // outside the tensor: the box reads as zeros
-    if (lane < ppt && (it.k0 * ppt + rel + lane) * p.P < it.valid_end) {
-      if (phys >= 0 && phys < p.num_pages)
-        outer = phys * p.Hkv + it.g;
-      else
-        record_error(kStatusBadInput, kKernPaged, 9, 1);
-    }
-    const int n = 2 * kt + which, s = n % NS;
-    if (n >= NS && !__all_sync(0xffffffffu, mbar_wait(&slot_empty[s], ((n / NS) - 1) & 1, abort_flag, kKernPaged, warp, 0)))
-      return false;
-    if (lane == 0) mbar_expect_tx(&slot_full[s], L::kTileBytes);
-    __syncwarp();
-    if (lane < ppt)
-      for (int c = 0; c < L::kChunks; ++c)
-        tma_load_3d(sRing + s * L::kTileBytes + c * L::kBoxBytes + lane * p.P * 128, which ? &p.tm_v : &p.tm_k,
-                    &slot_full[s], c * 64, 0, outer);
-    return true;
-  };
-  // tiles whose slot is empty from the start
-  const int early = (NS - which + 1) / 2;
-
   if (produces) {
     if (warp == 9 && lane == 0) {
       mbar_init(q_full, 1);
@@ -253,28 +229,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_paged_kernel(const __grid_c
       *abort_flag = 0;
       fence_mbar_init();
     }
-    if (lane == 0) prefetch_tensormap(which ? &p.tm_v : &p.tm_k);
+    if (lane == 0) prefetch_tensormap(warp == 10 ? &p.tm_v : &p.tm_k);
     named_barrier_sync(2, 64);
     named_barrier_arrive(3, kFwdThreads);  // the others wait for the barriers, not for the first loads
-    grid_dependency_wait();
-    it = paged_item(p);
-    grid_launch_dependents();
-    if (it.n_kv > 0) {
-      cur = entry(lane);
-      nxt = entry(32 + lane);
-      for (int kt = 0; kt < early && kt < it.n_kv; ++kt) {
-        load_tile(kt);
-        if (warp == 9 && kt == 0 && lane == 0) {
-          const int tiles = it.single ? 1 : 2;
-          mbar_expect_tx(q_full, static_cast<uint32_t>(tiles * L::kChunks * box_rows * 128));
-          for (int t = 0; t < tiles; ++t)
-            for (int c = 0; c < L::kChunks; ++c)
-              tma_load_5d(sQ + t * L::kTileBytes + c * L::kBoxBytes, &p.tm_q, q_full, c * 64, 0,
-                          p.decode ? 0 : (it.tile0 + t) * p.toks, it.g, p.decode ? (it.tile0 + t) * p.seqs : it.b);
-        }
-        __syncwarp();
-      }
-    }
   } else if (warp == 8) {
     tmem_alloc(tmem_ptr, 512);
     tmem_relinquish();
@@ -288,33 +245,74 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_paged_kernel(const __grid_c
     }
     fence_proxy_async_smem();
   }
+  grid_dependency_wait();
+  grid_launch_dependents();
+  uint32_t tmem = 0;
   if (!produces) {
-    grid_dependency_wait();
-    it = paged_item(p);
     tc_fence_before();
     named_barrier_sync(3, kFwdThreads);
     tc_fence_after();
+    tmem = *tmem_ptr;
   }
-  const uint32_t tmem = produces ? 0u : *tmem_ptr;
-  const bool single = it.single, dead = it.dead;
-  const int k0 = it.k0, n_kv = it.n_kv, valid_end = it.valid_end, owner = it.owner, split = it.split;
-  const int steps = single ? n_kv : 2 * n_kv;
 
+  const PagedItem it = paged_item(p);
+  const bool single = it.single;
   if (warp == 11) {
     // idle
   } else if (produces) {
-    bool ok = true;
-    int kt = early;
-    for (; ok && kt < n_kv; ++kt) ok = load_tile(kt);
-    // the copies in flight land before the block exits (at once, unless a
-    // wait ran out: the MMA warp waits for every tile)
-    if (n_kv > 0) {
-      if (warp == 9) mbar_wait_drain(q_full, 0, kKernPaged, 9, 2);
-      const int loaded = min(ok ? kt : kt - 1, n_kv);
-      for (int k = max(0, loaded - early); k < loaded; ++k) {
-        const int n = 2 * k + which;
-        if (n + NS >= 2 * n_kv)  // else the slot was filled again: it had landed
-          mbar_wait_drain(&slot_full[n % NS], (n / NS) & 1, kKernPaged, warp, 3);
+    // ------------------------------------------------------------ producers
+    // Warp 9 loads K tiles (and q), warp 10 V tiles.
+    const int which = warp - 9;
+    const int ppt = kPagedTile / p.P;  // pages of a key tile
+    if (it.n_kv > 0) {
+      const int* row = p.table + static_cast<size_t>(it.b) * p.max_pages;
+      const int n_pages = (it.valid_end + p.P - 1) / p.P, pg0 = it.k0 * ppt;
+      auto entry = [&](int rel) { return pg0 + rel < n_pages ? __ldg(row + pg0 + rel) : -1; };
+      int cur = entry(lane), nxt = entry(32 + lane);  // table entries of 32 pages, one a lane, and of the next 32
+      bool ok = true;
+      for (int kt = 0; kt < it.n_kv; ++kt) {
+        const int rel = kt * ppt;
+        if (kt > 0 && rel % 32 == 0) {
+          cur = nxt;
+          nxt = entry(rel + 32 + lane);
+        }
+        const int phys = __shfl_sync(0xffffffffu, cur, (rel + lane) & 31);
+        int outer = -1;  // outside the tensor: the box reads as zeros
+        if (lane < ppt && pg0 + rel + lane < n_pages) {
+          if (phys >= 0 && phys < p.num_pages)
+            outer = phys * p.Hkv + it.g;
+          else
+            record_error(kStatusBadInput, kKernPaged, 9, 1);
+        }
+        const int n = 2 * kt + which, s = n % NS;
+        if (n >= NS)
+          ok = __all_sync(0xffffffffu, mbar_wait(&slot_empty[s], ((n / NS) - 1) & 1, abort_flag, kKernPaged, warp, 0));
+        if (!ok) break;
+        if (lane == 0) mbar_expect_tx(&slot_full[s], L::kTileBytes);
+        __syncwarp();
+        if (lane < ppt)
+          for (int c = 0; c < L::kChunks; ++c)
+            tma_load_3d(sRing + s * L::kTileBytes + c * L::kBoxBytes + lane * p.P * 128, which ? &p.tm_v : &p.tm_k,
+                        &slot_full[s], c * 64, 0, outer);
+        if (which == 0 && kt == 0 && lane == 0) {
+          const int n_q = single ? 1 : 2;
+          mbar_expect_tx(q_full, static_cast<uint32_t>(n_q * L::kChunks * box_rows * 128));
+          for (int t = 0; t < n_q; ++t)
+            for (int c = 0; c < L::kChunks; ++c)
+              tma_load_5d(sQ + t * L::kTileBytes + c * L::kBoxBytes, &p.tm_q, q_full, c * 64, 0,
+                          p.decode ? 0 : (it.tile0 + t) * p.toks, it.g, p.decode ? (it.tile0 + t) * p.seqs : it.b);
+        }
+        __syncwarp();
+      }
+      // The copies in flight land before the block exits (at once, unless a
+      // wait ran out: the MMA warp waits for every tile).
+      if (ok) {
+        if (which == 0) mbar_wait_drain(q_full, 0, kKernPaged, 9, 2);
+        for (int k = max(0, it.n_kv - NS); k < it.n_kv; ++k) {
+          const int n = 2 * k + which;
+          if (n + NS >= 2 * it.n_kv)  // else the slot was filled again: it had landed
+            mbar_wait_drain(&slot_full[n % NS], (n / NS) & 1, kKernPaged, warp, 3);
+        }
       }
     }
   } else if (warp == 8) {
@@ -362,6 +360,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_paged_kernel(const __grid_c
       if (last_reader(i)) umma_commit_w(&slot_empty[s]);
       return true;
     };
+    const int steps = single ? it.n_kv : 2 * it.n_kv;
     if (steps > 0) {
       bool ok = wait_all(q_full, 0, 0);
       tc_fence_after();
@@ -389,11 +388,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_paged_kernel(const __grid_c
     const float c_log2 = p.scale_log2;
     const uint64_t c2 = f2pack(c_log2, c_log2);
     const int tile = single ? it.tile0 : it.tile0 + t;
-    const PagedRow row = paged_row(p, owner, tile, r);
+    const PagedRow row = paged_row(p, it.owner, tile, r);
     // last key the row sees; rows that are not written compute what they
     // find (a row never reaches another row's result)
     int lim = INT32_MAX;
-    bool write = row.in_tile && !dead;
+    bool write = row.in_tile && !it.dead;
     if (write) {
       const PagedSeq q = paged_seq(p, row.b);
       lim = q.live ? q.L - q.n + row.t : -1;
@@ -401,7 +400,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_paged_kernel(const __grid_c
       write = row.t < q.row_end;
     }
     const bool warp_works = __any_sync(0xffffffffu, write);
-    const int n_mine = single ? (n_kv + 1 - t) / 2 : n_kv;
+    const int n_mine = single ? (it.n_kv + 1 - t) / 2 : it.n_kv;
+    const int n_other = it.n_kv - n_mine;  // a single's other warpgroup
     float m_ref = -INFINITY, l_sum = 0.f;
     bool ok = true;
     auto load_s = [&](int kv0, uint32_t* s) {
@@ -445,8 +445,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_paged_kernel(const __grid_c
       }
       tc_fence_after();
       const int kt = single ? 2 * j + t : j;  // key tile of the block's range
-      const int kv0 = (k0 + kt) * kPagedTile;
-      if (kv0 + kPagedTile > valid_end && (single || t == 0)) {
+      const int kv0 = (it.k0 + kt) * kPagedTile;
+      if (kv0 + kPagedTile > it.valid_end && (single || t == 0)) {
         // the tile holds slots without a token: thread r clears value row r
         // if it is one (the first product on this value tile is this
         // warpgroup's, and waits for the arrivals below)
@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_paged_kernel(const __grid_c
           ok = false;
           break;
         }
-        if (kv0 + r >= valid_end) {
+        if (kv0 + r >= it.valid_end) {
 #pragma unroll
           for (int c = 0; c < L::kChunks; ++c)
 #pragma unroll
@@ -554,37 +554,18 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_paged_kernel(const __grid_c
     bool have = ok && n_mine > 0;
     if (have) have = mbar_wait(&pv_done[t], (n_mine - 1) & 1, abort_flag, kKernPaged, t, 2);
     have = __all_sync(0xffffffffu, have);
-    if (have) tc_fence_after();
     if (!have) m_ref = -INFINITY, l_sum = 0.f;
-    auto read_o = [&](int c, uint32_t* v) {
-      if (have) {
-        tmem_ld32(tm_O + c, v);
-        tmem_ld_wait();
-      } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = 0u;
-      }
-    };
-    // A single's two partial results meet in the ring (no product reads it
-    // any more once both warpgroups are here): warpgroup t finishes features
-    // t d/2 .. and leaves the others to the other, [d / 8][128] float4.
+    // A single's two partial results: tensor memory holds both in the same
+    // lanes, so each warpgroup joins and writes half of the features; only
+    // (m, l) go through shared memory.
     constexpr int kHalf = HD / 2;
-    float4* sO = reinterpret_cast<float4*>(sRing);
-    float2* sML = reinterpret_cast<float2*>(sRing + HD * 128 * 4);
     float w_own = 1.f, w_other = 0.f;
+    bool have_other = false;
     if (single) {
-      named_barrier_sync(1, 256);
       sML[t * 128 + r] = make_float2(m_ref, l_sum);
-#pragma unroll
-      for (int c = 0; c < kHalf; c += 32) {
-        uint32_t v[32];
-        read_o((1 - t) * kHalf + c, v);
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-          sO[(t * (kHalf / 4) + c / 4 + u) * 128 + r] =
-              make_float4(__uint_as_float(v[4 * u]), __uint_as_float(v[4 * u + 1]), __uint_as_float(v[4 * u + 2]),
-                          __uint_as_float(v[4 * u + 3]));
-      }
+      have_other = ok && n_other > 0;
+      if (have_other) have_other = mbar_wait(&pv_done[1 - t], (n_other - 1) & 1, abort_flag, kKernPaged, t, 4);
+      have_other = __all_sync(0xffffffffu, have_other);
       named_barrier_sync(1, 256);
       const float2 other = sML[(1 - t) * 128 + r];
       const float m = fmaxf(m_ref, other.x);
@@ -595,6 +576,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_paged_kernel(const __grid_c
       l_sum = l_sum * w_own + other.y * w_other;
       m_ref = m;
     }
+    if (have || have_other) tc_fence_after();
     const bool seen = l_sum > 0.f;
     const bool direct = p.part_o == nullptr;
     if (direct) {
@@ -602,7 +584,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_paged_kernel(const __grid_c
       w_own *= inv_l;
       w_other *= inv_l;
     }
-    const long long part = (static_cast<long long>(owner) * p.n_tiles + tile) * p.slots + split;
+    const long long part = (static_cast<long long>(it.owner) * p.n_tiles + tile) * p.slots + it.split;
     auto emit = [&](int c, const float* f) {  // features c .. c + 31 of the row
       if (direct) {
         T* orow = reinterpret_cast<T*>(p.o) + row.out * HD + c;
@@ -623,20 +605,22 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_paged_kernel(const __grid_c
     const int c_lo = single ? t * kHalf : 0, c_hi = single ? c_lo + kHalf : HD;
 #pragma unroll 2
     for (int c = c_lo; c < c_hi; c += 32) {
-      uint32_t v[32];
-      read_o(c, v);
       float f[32];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]) * w_own;
-      if (single) {
+      for (int i = 0; i < 32; ++i) f[i] = 0.f;
+      if (have) {
+        uint32_t v[32];
+        tmem_ld32(tm_O + c, v);
+        tmem_ld_wait();
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const float4 y = sO[((1 - t) * (kHalf / 4) + (c - c_lo) / 4 + u) * 128 + r];
-          f[4 * u] += y.x * w_other;
-          f[4 * u + 1] += y.y * w_other;
-          f[4 * u + 2] += y.z * w_other;
-          f[4 * u + 3] += y.w * w_other;
-        }
+        for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]) * w_own;
+      }
+      if (have_other) {
+        uint32_t v[32];
+        tmem_ld32(tmem + 256 + (1 - t) * 128 + lane_off + c, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) f[i] = fmaf(__uint_as_float(v[i]), w_other, f[i]);
       }
       if (write) emit(c, f);
     }
