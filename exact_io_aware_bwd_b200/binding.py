@@ -387,10 +387,6 @@ def fa_decode_paged(q, k_cache, v_cache, block_table, seq_lens, o, lse, scale: f
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _dense(t, shape, dtype, dev):
-    return t.shape == shape and t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
-
-
 def _fits(where, dev, *spec):
     """Says what is wrong: each (name, tensor, shape, dtype) must have the
     shape and dtype (None: any), a dense layout and CUDA device `dev`; those
@@ -446,22 +442,12 @@ def _launch(fn, where, dev, stream, args):
         raise FaError(st, where)
 
 
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _row_strides(where, name, t, shape, dtype, dev):
+def _row_strides(where, name, t):
     """(batch, head, token) strides of a [B, H, N, d] tensor whose rows are
     contiguous; a dimension of one entry or none is never stepped over."""
-    if t.shape != shape:
-        raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype is not dtype:
-        raise TypeError(f"{where}: {name} has dtype {t.dtype}, expected {dtype}")
-    if t.stride(3) != 1 and shape[3] > 1:
+    (b, h, n, d), (sb, sh, sn, sd) = t.shape, t.stride()
+    if sd != 1 and d > 1:
         raise ValueError(f"{where}: the rows of {name} must be contiguous")
-    if dev >= 0 and t.get_device() != dev:
-        raise ValueError(f"{where}: all tensors must be on one device ({name} is on {t.device})")
-    (b, h, n, _), (sb, sh, sn, _) = shape, t.stride()
     return sb if b > 1 else 0, sh if h > 1 else 0, sn if n > 1 else 0
 
 
@@ -477,79 +463,132 @@ def fa_append_paged(q, k, v, q_out, k_out, k_cache, v_cache, block_table, seq_le
     which sequence b has new_lens[b] (None: N); inv_freq fp32 [rot/2] or None
     (no rotation)."""
     where = "fa_append_paged"
+    try:
+        dt, dev, kv = k.dtype, k.get_device(), k.shape
+        cache, lens = k_cache.shape, seq_lens.shape
+        B, Hkv, N, d = kv
+        num_pages, Hc, P, dc = cache
+        Bt, max_pages = block_table.shape
+        i32, rot, Hq = torch.int32, 0, Hkv
+        fine = (dev >= 0 and Hc == Hkv and dc == d and Bt == B and lens == (B,) and v.shape == kv and v.dtype is dt
+                and v.get_device() == dev and v_cache.shape == cache and k_cache.dtype is dt and v_cache.dtype is dt
+                and k_cache.get_device() == dev and v_cache.get_device() == dev and k_cache.is_contiguous()
+                and v_cache.is_contiguous() and block_table.dtype is i32 and seq_lens.dtype is i32
+                and block_table.get_device() == dev and seq_lens.get_device() == dev and block_table.is_contiguous()
+                and seq_lens.is_contiguous())
+        dense = k.is_contiguous() and v.is_contiguous()
+        if q is not None:
+            Bq, Hq, Nq, dq = qs = q.shape
+            fine = (fine and Bq == B and Nq == N and dq == d and q.dtype is dt and q.get_device() == dev
+                    and q_out.shape == qs and q_out.dtype is dt and q_out.get_device() == dev and q_out.is_contiguous())
+            dense = dense and q.is_contiguous()
+        elif q_out is not None:
+            fine = False
+        if new_lens is not None:
+            fine = (fine and new_lens.shape == lens and new_lens.dtype is i32 and new_lens.get_device() == dev
+                    and new_lens.is_contiguous())
+        if k_out is not None:
+            fine = (fine and k_out.shape == kv and k_out.dtype is dt and k_out.get_device() == dev
+                    and k_out.is_contiguous())
+        if inv_freq is not None:
+            rot = 2 * inv_freq.numel()
+            fine = (fine and inv_freq.dim() == 1 and inv_freq.dtype is torch.float32 and inv_freq.get_device() == dev
+                    and inv_freq.is_contiguous())
+        dtype_code = _DTYPES[dt]
+    except (AttributeError, KeyError, TypeError, ValueError):  # not a tensor, another type or number of dimensions
+        fine = False
+    if not fine:
+        _refuse_append(where, q, k, v, q_out, k_out, k_cache, v_cache, block_table, seq_lens, new_lens, inv_freq)
+    strides = None
+    if not dense:
+        strides = _NineStrides(*((0, 0, 0) if q is None else _row_strides(where, "q", q)), *_row_strides(where, "k", k),
+                               *_row_strides(where, "v", v))
+    _launch((_lib or load()).fa_append_paged, where, dev, stream,
+            (None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(), strides,
+             None if q is None else q_out.data_ptr(), None if k_out is None else k_out.data_ptr(), k_cache.data_ptr(),
+             v_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+             None if new_lens is None else new_lens.data_ptr(), None if inv_freq is None else inv_freq.data_ptr(),
+             B, Hq, Hkv, N, d, P, max_pages, num_pages, rot, 1 if interleaved else 0, dtype_code))
+
+
+def _refuse_append(where, q, k, v, q_out, k_out, k_cache, v_cache, block_table, seq_lens, new_lens, inv_freq):
+    """Raises what is wrong with the arguments of fa_append_paged."""
     if (q is None) != (q_out is None):
         raise ValueError(f"{where}: q and q_out come together")
-    _four_d(where, ("k", k), ("v", v), ("k_cache", k_cache))
+    named = (("k", k), ("v", v), ("k_cache", k_cache)) + ((("q", q),) if q is not None else ())
+    _four_d(where, *named)
     dt, dev = k.dtype, k.get_device()
     if dt not in _DTYPES:
         raise TypeError(f"{where}: k has dtype {dt}, expected bfloat16 or float16")
-    B, Hkv, N, d = kv_shape = k.shape
-    Hq, q_shape = Hkv, None
-    if q is not None:
-        _four_d(where, ("q", q))
-        Hq = q.shape[1]
-        q_shape = (B, Hq, N, d)
-    strides = None
-    if not (k.is_contiguous() and _dense(v, kv_shape, dt, dev) and (q is None or _dense(q, q_shape, dt, dev))):
-        strides = _NineStrides(*([0, 0, 0] if q is None else _row_strides(where, "q", q, q_shape, dt, dev)),
-                               *_row_strides(where, "k", k, kv_shape, dt, dev),
-                               *_row_strides(where, "v", v, kv_shape, dt, dev))
-    rot = 0
-    if inv_freq is not None:
-        if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
-            raise ValueError(f"{where}: inv_freq must be a 1-D tensor")
-        rot = 2 * inv_freq.shape[0]
+    B, Hkv, N, d = kv = k.shape
+    q_shape = None if q is None else (B, q.shape[1], N, d)
+    for name, t, shape in (("q", q, q_shape), ("v", v, kv)):
+        if t is not None and t.shape != shape:
+            raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if t is not None and t.dtype is not dt:
+            raise TypeError(f"{where}: {name} has dtype {t.dtype}, expected {dt}")
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if t is not None:
+            _row_strides(where, name, t)
+    if inv_freq is not None and (not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1):
+        raise ValueError(f"{where}: inv_freq must be a 1-D tensor")
     num_pages, Hc, P, _ = k_cache.shape
     if Hc != Hkv:
         raise ValueError(f"{where}: k has {Hkv} heads, the cache {Hc}")
-    max_pages = _table_width(where, block_table)
-    i32, cache = torch.int32, (num_pages, Hkv, P, d)
-    try:
-        fine = (dev >= 0 and _dense(k_cache, cache, dt, dev) and _dense(v_cache, cache, dt, dev)
-                and _dense(block_table, (B, max_pages), i32, dev) and _dense(seq_lens, (B,), i32, dev)
-                and (new_lens is None or _dense(new_lens, (B,), i32, dev))
-                and (q is None or _dense(q_out, q_shape, dt, dev)) and (k_out is None or _dense(k_out, kv_shape, dt, dev))
-                and (rot == 0 or _dense(inv_freq, (rot // 2,), torch.float32, dev)))
-    except AttributeError:  # not a tensor
-        fine = False
-    if not fine:
-        _fits(where, dev, ("k_cache", k_cache, cache, dt), ("v_cache", v_cache, cache, dt),
-              ("block_table", block_table, (B, max_pages), i32), ("seq_lens", seq_lens, (B,), i32),
-              ("new_lens", new_lens, (B,), i32), ("q_out", q_out, q_shape, dt), ("k_out", k_out, kv_shape, dt),
-              ("inv_freq", inv_freq, None, torch.float32))
-    _launch((_lib or load()).fa_append_paged, where, dev, stream,
-            (_addr(q), k.data_ptr(), v.data_ptr(), strides, _addr(q_out), _addr(k_out), k_cache.data_ptr(),
-             v_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), _addr(new_lens), _addr(inv_freq), B, Hq,
-             Hkv, N, d, P, max_pages, num_pages, rot, 1 if interleaved else 0, _DTYPES[dt]))
+    max_pages, cache = _table_width(where, block_table), (num_pages, Hkv, P, d)
+    _fits(where, dev, ("k_cache", k_cache, cache, dt), ("v_cache", v_cache, cache, dt),
+          ("block_table", block_table, (B, max_pages), torch.int32), ("seq_lens", seq_lens, (B,), torch.int32),
+          ("new_lens", new_lens, (B,), torch.int32), ("q_out", q_out, q_shape, dt), ("k_out", k_out, kv, dt),
+          ("inv_freq", inv_freq, None, torch.float32))
+    for name, t in (("q", q), ("v", v)):
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{where}: all tensors must be on one device ({name} is on {t.device})")
+    raise ValueError(f"{where}: arguments do not fit together")
 
 
 def _attention_paged(where, q, k_cache, v_cache, block_table, seq_lens, new_lens, o, lse, workspace):
     """Checks shared by the attention passes over the cache; returns the
     device, the library's pointer and size arguments, and the workspace's."""
-    _four_d(where, ("q", q), ("k_cache", k_cache))
-    dt, dev = q.dtype, q.get_device()
-    if dt not in _DTYPES:
-        raise TypeError(f"{where}: q has dtype {dt}, expected bfloat16 or float16")
-    B, Hq, N, d = q_shape = q.shape
-    num_pages, Hkv, P, _ = k_cache.shape
-    max_pages = _table_width(where, block_table)
-    i32, cache = torch.int32, (num_pages, Hkv, P, d)
     try:
-        fine = (dev >= 0 and q.is_contiguous() and _dense(k_cache, cache, dt, dev) and _dense(v_cache, cache, dt, dev)
-                and _dense(block_table, (B, max_pages), i32, dev) and _dense(seq_lens, (B,), i32, dev)
-                and (new_lens is None or _dense(new_lens, (B,), i32, dev)) and _dense(o, q_shape, dt, dev)
-                and _dense(lse, (B, Hq, N), torch.float32, dev)
-                and (workspace is None or (workspace.is_contiguous() and workspace.get_device() == dev)))
-    except AttributeError:  # not a tensor
+        dt, dev, qs = q.dtype, q.get_device(), q.shape
+        cache, lens = k_cache.shape, seq_lens.shape
+        B, Hq, N, d = qs
+        num_pages, Hkv, P, dc = cache
+        Bt, max_pages = block_table.shape
+        i32 = torch.int32
+        fine = (dev >= 0 and dc == d and Bt == B and lens == (B,) and v_cache.shape == cache and o.shape == qs
+                and lse.shape == (B, Hq, N) and k_cache.dtype is dt and v_cache.dtype is dt and o.dtype is dt
+                and lse.dtype is torch.float32 and block_table.dtype is i32 and seq_lens.dtype is i32
+                and k_cache.get_device() == dev and v_cache.get_device() == dev and block_table.get_device() == dev
+                and seq_lens.get_device() == dev and o.get_device() == dev and lse.get_device() == dev
+                and q.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous()
+                and block_table.is_contiguous() and seq_lens.is_contiguous() and o.is_contiguous()
+                and lse.is_contiguous())
+        if new_lens is not None:
+            fine = (fine and new_lens.shape == lens and new_lens.dtype is i32 and new_lens.get_device() == dev
+                    and new_lens.is_contiguous())
+        ws = (None, 0)
+        if workspace is not None:
+            fine = fine and workspace.get_device() == dev and workspace.is_contiguous()
+            ws = (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+        dtype_code = _DTYPES[dt]
+    except (AttributeError, KeyError, TypeError, ValueError):  # not a tensor, another type or number of dimensions
         fine = False
     if not fine:
-        _fits(where, dev, ("q", q, q_shape, dt), ("k_cache", k_cache, cache, dt), ("v_cache", v_cache, cache, dt),
-              ("block_table", block_table, (B, max_pages), i32), ("seq_lens", seq_lens, (B,), i32),
-              ("new_lens", new_lens, (B,), i32), ("o", o, q_shape, dt), ("lse", lse, (B, Hq, N), torch.float32),
+        _four_d(where, ("q", q), ("k_cache", k_cache))
+        dt, dev = q.dtype, q.get_device()
+        if dt not in _DTYPES:
+            raise TypeError(f"{where}: q has dtype {dt}, expected bfloat16 or float16")
+        B, Hq, N, d = q.shape
+        num_pages, Hkv, P, _ = k_cache.shape
+        max_pages, cache = _table_width(where, block_table), (num_pages, Hkv, P, d)
+        _fits(where, dev, ("q", q, q.shape, dt), ("k_cache", k_cache, cache, dt), ("v_cache", v_cache, cache, dt),
+              ("block_table", block_table, (B, max_pages), torch.int32), ("seq_lens", seq_lens, (B,), torch.int32),
+              ("new_lens", new_lens, (B,), torch.int32), ("o", o, q.shape, dt), ("lse", lse, (B, Hq, N), torch.float32),
               ("workspace", workspace, None, None))
+        raise ValueError(f"{where}: arguments do not fit together")
     tensors = (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr())
-    ws = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    return dev, tensors, (o.data_ptr(), lse.data_ptr()), (B, Hq, Hkv, N, d, P, max_pages, num_pages), _DTYPES[dt], ws
+    return dev, tensors, (o.data_ptr(), lse.data_ptr()), (B, Hq, Hkv, N, d, P, max_pages, num_pages), dtype_code, ws
 
 
 def fa_fwd_paged_workspace_bytes(B: int, Hq: int, Hkv: int, N: int, d: int, page_size: int, max_pages: int) -> int:
@@ -565,7 +604,8 @@ def fa_fwd_paged(q, k_cache, v_cache, block_table, seq_lens, new_lens, o, lse, s
     where = "fa_fwd_paged"
     dev, ins, outs, sizes, dt, ws = _attention_paged(where, q, k_cache, v_cache, block_table, seq_lens, new_lens, o, lse,
                                                      workspace)
-    _launch((_lib or load()).fa_fwd_paged, where, dev, stream, (*ins, _addr(new_lens), *outs, *sizes, scale, dt, *ws))
+    _launch((_lib or load()).fa_fwd_paged, where, dev, stream,
+            (*ins, None if new_lens is None else new_lens.data_ptr(), *outs, *sizes, scale, dt, *ws))
 
 
 def fa_decode_prefix_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, d: int, page_size: int, max_pages: int,
