@@ -782,6 +782,7 @@ bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 struct PagedPlan {
   int toks, seqs;   // a row tile: tokens x sequences (x G heads)
   int n_tiles;      // row tiles of an owner
+  int n_pairs;      // the first 2 n_pairs of them in pairs, the others one by one
   int64_t owners;   // kv heads, of every sequence in the forward pass
   int S, S_single;  // key splits of a pair of row tiles / of an odd last one
   bool joined;      // partial results go through the workspace
@@ -805,14 +806,17 @@ PagedPlan paged_plan(int B, int Hq, int Hkv, int N, int d, int64_t keys, bool pr
   pl.n_tiles = prefix ? (B + pl.seqs - 1) / pl.seqs : (N + pl.toks - 1) / pl.toks;
   pl.owners = prefix ? Hkv : static_cast<int64_t>(B) * Hkv;
   if (prefix && keys == 0) {  // nothing shared: no blocks, no partial results
-    pl.S = pl.S_single = 0;
+    pl.n_pairs = pl.S = pl.S_single = 0;
     pl.joined = true;
     return pl;
   }
-  const int64_t pairs = pl.n_tiles / 2, odd = pl.n_tiles % 2;
   const int64_t tiles = std::max<int64_t>(1, (keys + 127) / 128);
   const int64_t cap = std::min<int64_t>(fa::kDecodeSMs, std::max<int64_t>(1, tiles / 2));
+  // row tiles one by one while even so they do not fill the GPU (a pair reads
+  // each key once for both)
+  const int64_t pairs = pl.owners * pl.n_tiles > fa::kDecodeSMs ? pl.n_tiles / 2 : 0, odd = pl.n_tiles - 2 * pairs;
   double best = 1e300;
+  pl.n_pairs = static_cast<int>(pairs);
   pl.S = pl.S_single = 1;
   for (int64_t S = 1; S <= cap; ++S) {
     const int64_t Ss = odd ? (pairs ? (S + 1) / 2 : S) : 1;
@@ -913,11 +917,12 @@ fa_status_t paged_run(const PagedArgs& a, const PagedPlan& pl, void* workspace, 
   prm.toks = pl.toks;
   prm.seqs = pl.seqs;
   prm.n_tiles = pl.n_tiles;
+  prm.n_pairs = pl.n_pairs;
   prm.S = pl.S;
   prm.S_single = pl.S_single;
   prm.slots = pl.slots();
   prm.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
-  const int64_t blocks = pl.owners * (static_cast<int64_t>(pl.n_tiles / 2) * pl.S + (pl.n_tiles % 2) * pl.S_single);
+  const int64_t blocks = pl.owners * (static_cast<int64_t>(pl.n_pairs) * pl.S + static_cast<int64_t>(pl.n_tiles - 2 * pl.n_pairs) * pl.S_single);
   if (blocks > INT32_MAX) return FA_ERR_UNSUPPORTED;
   auto run = [&](auto kern, auto own1, auto own2, auto merge, int smem) -> fa_status_t {
     fa_status_t r = opt_in_smem(kern, smem);

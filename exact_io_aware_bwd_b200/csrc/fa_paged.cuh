@@ -15,8 +15,9 @@
 // Either is one box of a 5-D tensor map over q (feature, head of the group,
 // token, kv head, sequence).
 //
-// A thread block takes two row tiles of a kv head (a pair) or, when the count
-// is odd, the last one alone, and a range of 128-key tiles:
+// A thread block takes two row tiles of a kv head (a pair) or one (the last of
+// an odd number, and each while there are too few to fill the GPU), and a
+// range of 128-key tiles:
 //   pair      row tile t belongs to softmax warpgroup t, both read every key
 //             tile: step i is row tile i & 1 on key tile i >> 1;
 //   single    both warpgroups hold the same rows and take turns on the key
@@ -67,6 +68,7 @@ struct PagedParams {
   int prefix;           // keys of the shared prefix
   int toks, seqs;       // a row tile: tokens x sequences (x G heads)
   int n_tiles;          // row tiles of an owner (kv head, of a sequence in the forward pass)
+  int n_pairs;          // the first 2 n_pairs of them in pairs, the others as singles
   int S, S_single;      // key splits of a pair / of a single
   int slots;            // the larger of the two
   float scale_log2;
@@ -117,7 +119,7 @@ __device__ __forceinline__ PagedRow paged_row(const PagedParams& p, int owner, i
 struct PagedItem {
   bool single;  // one row tile, its key tiles shared out between the warpgroups
   bool dead;    // only padding rows: nothing is written
-  int split, owner, tile0, g, b;
+  int split, splits, owner, tile0, g, b;
   int valid_end;  // keys that hold a token
   int k0, n_kv;   // key tiles
 };
@@ -128,15 +130,19 @@ __device__ __forceinline__ PagedItem paged_item(const PagedParams& p) {
   PagedItem it;
   int x = blockIdx.x;
   const int owners = p.decode ? p.Hkv : p.B * p.Hkv;
-  const int n_pairs = p.n_tiles / 2;
-  it.single = x >= n_pairs * owners * p.S;
-  if (it.single) x -= n_pairs * owners * p.S;
-  const int splits = it.single ? p.S_single : p.S;
-  it.split = x % splits;
-  it.owner = (x / splits) % owners;
-  it.tile0 = it.single ? p.n_tiles - 1 : 2 * (n_pairs - 1 - x / (splits * owners));
+  it.single = x >= p.n_pairs * owners * p.S;
+  if (it.single) x -= p.n_pairs * owners * p.S;
+  it.splits = it.single ? p.S_single : p.S;
+  it.split = x % it.splits;
+  it.owner = (x / it.splits) % owners;
+  it.tile0 = it.single ? p.n_tiles - 1 - x / (it.splits * owners) : 2 * (p.n_pairs - 1 - x / (it.splits * owners));
   it.g = it.owner % p.Hkv;
   it.b = p.decode ? 0 : it.owner / p.Hkv;
+  return it;
+}
+
+// What of it depends on the sequence's lengths.
+__device__ __forceinline__ void paged_item_keys(const PagedParams& p, PagedItem& it) {
   it.dead = false;
   int keys;  // keys some row of the item sees
   if (p.decode) {
@@ -150,9 +156,8 @@ __device__ __forceinline__ PagedItem paged_item(const PagedParams& p) {
     it.valid_end = q.L;
   }
   const int n = (keys + kPagedTile - 1) / kPagedTile;
-  it.k0 = static_cast<int>(static_cast<long long>(n) * it.split / splits);
-  it.n_kv = static_cast<int>(static_cast<long long>(n) * (it.split + 1) / splits) - it.k0;
-  return it;
+  it.k0 = static_cast<int>(static_cast<long long>(n) * it.split / it.splits);
+  it.n_kv = static_cast<int>(static_cast<long long>(n) * (it.split + 1) / it.splits) - it.k0;
 }
 
 // Arrives on a named barrier without waiting for it.
@@ -255,8 +260,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_paged_kernel(const __grid_c
     tmem = *tmem_ptr;
   }
 
-  const PagedItem it = paged_item(p);
+  PagedItem it = paged_item(p);
   const bool single = it.single;
+  // unsplit, the first table entries are asked for before the length is known
+  const int* row_table = p.table + static_cast<size_t>(it.b) * p.max_pages;
+  int cur = -1, nxt = -1;  // table entries of 32 pages, one a lane, and of the next 32
+  if (produces && it.splits == 1) {
+    if (lane < p.max_pages) cur = __ldg(row_table + lane);
+    if (lane + 32 < p.max_pages) nxt = __ldg(row_table + lane + 32);
+  }
+  paged_item_keys(p, it);
   if (warp == 11) {
     // idle
   } else if (produces) {
@@ -265,10 +278,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_paged_kernel(const __grid_c
     const int which = warp - 9;
     const int ppt = kPagedTile / p.P;  // pages of a key tile
     if (it.n_kv > 0) {
-      const int* row = p.table + static_cast<size_t>(it.b) * p.max_pages;
       const int n_pages = (it.valid_end + p.P - 1) / p.P, pg0 = it.k0 * ppt;
-      auto entry = [&](int rel) { return pg0 + rel < n_pages ? __ldg(row + pg0 + rel) : -1; };
-      int cur = entry(lane), nxt = entry(32 + lane);  // table entries of 32 pages, one a lane, and of the next 32
+      auto entry = [&](int rel) { return pg0 + rel < n_pages ? __ldg(row_table + pg0 + rel) : -1; };
+      if (it.splits > 1) cur = entry(lane), nxt = entry(32 + lane);
       bool ok = true;
       for (int kt = 0; kt < it.n_kv; ++kt) {
         const int rel = kt * ppt;
@@ -585,12 +597,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_paged_kernel(const __grid_c
       w_other *= inv_l;
     }
     const long long part = (static_cast<long long>(it.owner) * p.n_tiles + tile) * p.slots + it.split;
+    // the rows of a tile in the I/O type, staged where q was: 16-byte pieces
+    // swizzled by row (d / 8 of them; a single's half: d / 16)
+    uint8_t* sOut = sQ + t * L::kTileBytes + r * (HD * 2);
     auto emit = [&](int c, const float* f) {  // features c .. c + 31 of the row
       if (direct) {
-        T* orow = reinterpret_cast<T*>(p.o) + row.out * HD + c;
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-          *reinterpret_cast<uint4*>(orow + 8 * u) =
+          *reinterpret_cast<uint4*>(sOut + (((c / 8 + u) ^ (r & 7)) << 4)) =
               make_uint4(pack2<BF16>(f[8 * u], f[8 * u + 1]), pack2<BF16>(f[8 * u + 2], f[8 * u + 3]),
                          pack2<BF16>(f[8 * u + 4], f[8 * u + 5]), pack2<BF16>(f[8 * u + 6], f[8 * u + 7]));
       } else {
@@ -623,6 +637,21 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_paged_kernel(const __grid_c
         for (int i = 0; i < 32; ++i) f[i] = fmaf(__uint_as_float(v[i]), w_other, f[i]);
       }
       if (write) emit(c, f);
+    }
+    if (direct) {
+      // A row's 16-byte pieces by neighbouring lanes: whole lines (a thread
+      // writing its own row touched 32 lines an instruction, 1.6 us a tile).
+      __syncwarp();
+      const int pieces = single ? HD / 16 : HD / 8, rows = 32 / pieces;
+      const int piece = (single ? t * (HD / 16) : 0) + lane % pieces, r0 = lane / pieces;
+      const uint8_t* src = sQ + t * L::kTileBytes + (r & ~31) * (HD * 2);
+      for (int i = 0; i < 32; i += rows) {
+        const int x = i + r0;
+        const long long out = __shfl_sync(0xffffffffu, row.out, x);
+        if (__shfl_sync(0xffffffffu, write ? 1 : 0, x))
+          *reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.o) + out * HD + piece * 8) =
+              *reinterpret_cast<const uint4*>(src + x * (HD * 2) + ((piece ^ (x & 7)) << 4));
+      }
     }
     if (write && !(single && t == 1)) {
       if (direct)
@@ -668,7 +697,7 @@ __global__ void __launch_bounds__(256) fa_paged_merge_kernel(const __grid_consta
   if (!row.in_tile) return;
   const PagedSeq q = paged_seq(p, row.b);
   if (row.t >= q.row_end) return;
-  const bool single = (p.n_tiles & 1) && tile == p.n_tiles - 1;
+  const bool single = tile >= 2 * p.n_pairs;
   const int S = single ? p.S_single : p.S;
   const long long part = (static_cast<long long>(owner) * p.n_tiles + tile) * p.slots;
   const float2* ml = p.part_ml + part * 128 + r;

@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(kOwnThreads, own_blocks_per_sm(HD)) fa_prefix_
   // Weights of a row's partial results: a warp takes rows in turn, its lanes
   // the prefix's splits.
   const int tile = b / p.seqs;
-  const bool single = (p.n_tiles & 1) && tile == p.n_tiles - 1;
+  const bool single = tile >= 2 * p.n_pairs;
   const int slots = last ? (single ? p.S_single : p.S) : 0;  // 0 without a prefix
   const long long part = (static_cast<long long>(g) * p.n_tiles + tile) * p.slots;
   auto tile_row = [&](int r) {  // of the prefix's tile: (sequence, token, head)
