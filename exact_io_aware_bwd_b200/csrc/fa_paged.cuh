@@ -23,8 +23,8 @@
 //   single    both warpgroups hold the same rows and take turns on the key
 //             tiles: step i is warpgroup i & 1 on key tile i; their two
 //             partial results are joined in shared memory at the end.
-// The tensor cores run S_i+2 right after O += P_i V: one warpgroup's softmax
-// overlaps the other's products in both forms.
+// The tensor cores run the scores two or three steps ahead: one warpgroup's
+// softmax overlaps the other's products in both forms.
 //
 // When there are too few blocks to fill the GPU the key tiles of a row tile are
 // split over several blocks, each leaving unnormalised O with its reference
@@ -181,7 +181,14 @@ __device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, u
 template <int HD>
 struct PagedLayout : FwdLayout<HD> {
   static constexpr int kOffML = (FwdLayout<HD>::kSmemBytes + 15) / 16 * 16;
-  static constexpr int kBytes = kOffML + 2 * 128 * 8;
+  // Score buffers in tensor memory, 128 columns each, then the two O tiles: a
+  // third one fits at d = 64, and lets S run three steps ahead of P V, so that
+  // a warpgroup finds its next scores ready (two ahead, it waits for its own P
+  // V first: 0.95 us a step, 1.1 us of softmax and 0.8 us of products in turn
+  // on each of two warpgroups).
+  static constexpr int kDepth = HD == 64 ? 3 : 2;
+  static constexpr int kOffStep = kOffML + 2 * 128 * 8;  // s_full[kDepth], p_half[kDepth][2]
+  static constexpr int kBytes = kOffStep + 3 * kDepth * 8;
   static_assert(kBytes <= 232448, "shared memory budget");
 };
 
@@ -198,10 +205,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_paged_kernel(const __grid_c
   uint64_t* q_full = bars;
   uint64_t* slot_full = bars + 1;
   uint64_t* slot_empty = slot_full + NS;
-  uint64_t* s_full = slot_empty + NS;
-  uint64_t* p_half = s_full + 2;  // [warpgroup][half]
-  uint64_t* pv_done = p_half + 4;
+  uint64_t* pv_done = slot_empty + NS;  // [warpgroup]
   uint64_t* done_bar = pv_done + 2;
+  constexpr int kDepth = L::kDepth;
+  constexpr uint32_t kColO = kDepth * 128;
+  uint64_t* s_full = reinterpret_cast<uint64_t*>(sm + L::kOffStep);  // [buffer]
+  uint64_t* p_half = s_full + kDepth;                                // [buffer][half]
   float2* sML = reinterpret_cast<float2*>(sm + L::kOffML);
   uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(sm + L::kOffTmemPtr);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::kOffAbort);
@@ -224,12 +233,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_paged_kernel(const __grid_c
         mbar_init(&slot_full[s], 1);
         mbar_init(&slot_empty[s], 1);
       }
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < kDepth; ++i) {
         mbar_init(&s_full[i], 1);
         mbar_init(&p_half[2 * i], 128);
         mbar_init(&p_half[2 * i + 1], 128);
-        mbar_init(&pv_done[i], 1);
       }
+      mbar_init(&pv_done[0], 1);
+      mbar_init(&pv_done[1], 1);
       mbar_init(done_bar, 1);
       *abort_flag = 0;
       fence_mbar_init();
@@ -342,30 +352,30 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_paged_kernel(const __grid_c
     // the last step that reads a key tile hands its slots back
     auto last_reader = [&](int i) { return single || (i & 1) != 0; };
     auto issue_s = [&](int i) -> bool {
-      const int n = ring(i), s = n % NS, t = i & 1;
+      const int n = ring(i), s = n % NS, t = i & 1, buf = i % kDepth;
       if (!wait_all(&slot_full[s], (n / NS) & 1, 1)) return false;
       tc_fence_after();
       const uint32_t qo = single ? 0u : t * L::kTileBytes, ko = s * L::kTileBytes;
 #pragma unroll
       for (int k = 0; k < HD / 16; ++k) {
         const uint32_t off = (k >> 2) * L::kBoxBytes + (k & 3) * 32;
-        umma_ss_w(tmem + t * 128, sdesc_add(dQ_k, qo + off), sdesc_add(dR_k, ko + off), kIdS, k > 0);
+        umma_ss_w(tmem + buf * 128, sdesc_add(dQ_k, qo + off), sdesc_add(dR_k, ko + off), kIdS, k > 0);
       }
-      umma_commit_w(&s_full[t]);
+      umma_commit_w(&s_full[buf]);
       if (last_reader(i)) umma_commit_w(&slot_empty[s]);
       return true;
     };
     auto issue_pv = [&](int i) -> bool {
-      const int n = ring(i) + 1, s = n % NS, t = i & 1, j = i >> 1;
+      const int n = ring(i) + 1, s = n % NS, t = i & 1, j = i >> 1, buf = i % kDepth;
       if (!wait_all(&slot_full[s], (n / NS) & 1, 2)) return false;
       const uint32_t vo = s * L::kTileBytes;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        if (!wait_all(&p_half[2 * t + half], j & 1, 3)) return false;
+        if (!wait_all(&p_half[2 * buf + half], (i / kDepth) & 1, 3)) return false;
         tc_fence_after();
 #pragma unroll
         for (int k = 4 * half; k < 4 * half + 4; ++k)
-          umma_ts_w(tmem + 256 + t * 128, tmem + t * 128 + k * 8, sdesc_add(dR_mn, vo + k * 2048), kIdPV,
+          umma_ts_w(tmem + kColO + t * HD, tmem + buf * 128 + k * 8, sdesc_add(dR_mn, vo + k * 2048), kIdPV,
                     (j > 0 || k > 0) ? 1u : 0u);
       }
       umma_commit_w(&pv_done[t]);
@@ -376,13 +386,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_paged_kernel(const __grid_c
     if (steps > 0) {
       bool ok = wait_all(q_full, 0, 0);
       tc_fence_after();
-      // S_0 S_1 | P_0 V, S_2 | P_1 V, S_3 | ...  S_i+2 overwrites the tensor
-      // memory that O += P_i V reads P_i from; the tensor core runs one
-      // thread's MMAs in issue order, so no wait is put between them.  (One
+      // S_0 S_1 | P_0 V, S_2 | P_1 V, S_3 | ... (two ahead; three at d = 64).
+      // S overwrites the tensor memory that the O += P V before it reads P
+      // from; the tensor core runs one thread's MMAs in issue order, so no wait
+      // is put between them.  (One
       // copy of each in the code: a cold instruction line costs microseconds
       // while every block's first loads are in flight.)
-      for (int i = 0; ok && i < steps + 2; ++i) {
-        if (i >= 2) ok = issue_pv(i - 2);
+      for (int i = 0; ok && i < steps + kDepth; ++i) {
+        if (i >= kDepth) ok = issue_pv(i - kDepth);
         if (ok && i < steps) ok = issue_s(i);
       }
     }
@@ -395,8 +406,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_paged_kernel(const __grid_c
     const int t = warp >> 2;    // warpgroup
     const int r = tid & 127;    // row within the tile == tensor-memory lane
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tm_S = tmem + t * 128 + lane_off;
-    const uint32_t tm_O = tmem + 256 + t * 128 + lane_off;
+    uint32_t tm_S = tmem + t * 128 + lane_off;  // the step's score buffer
+    const uint32_t tm_O = tmem + kColO + t * HD + lane_off;
+    int buf = t;
     const float c_log2 = p.scale_log2;
     const uint64_t c2 = f2pack(c_log2, c_log2);
     const int tile = single ? it.tile0 : it.tile0 + t;
@@ -444,14 +456,20 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_paged_kernel(const __grid_c
     auto hand_over = [&](int half) {
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(&p_half[2 * t + half]);
+      mbar_arrive(&p_half[2 * buf + half]);
     };
     auto sum_acc = [&](const uint64_t* acc) {
       const uint64_t a = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
       return f2lo(a) + f2hi(a);
     };
     for (int j = 0; j < n_mine; ++j) {
-      if (!__all_sync(0xffffffffu, mbar_wait(&s_full[t], j & 1, abort_flag, kKernPaged, t, 0))) {
+      uint32_t use = j;  // how often the buffer was used before
+      if constexpr (kDepth != 2) {
+        buf = (2 * j + t) % kDepth;
+        use = (2 * j + t) / kDepth;
+        tm_S = tmem + buf * 128 + lane_off;
+      }
+      if (!__all_sync(0xffffffffu, mbar_wait(&s_full[buf], use & 1, abort_flag, kKernPaged, t, 0))) {
         ok = false;
         break;
       }
@@ -631,7 +649,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_paged_kernel(const __grid_c
       }
       if (have_other) {
         uint32_t v[32];
-        tmem_ld32(tmem + 256 + (1 - t) * 128 + lane_off + c, v);
+        tmem_ld32(tmem + kColO + (1 - t) * HD + lane_off + c, v);
         tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 32; ++i) f[i] = fmaf(__uint_as_float(v[i]), w_other, f[i]);
