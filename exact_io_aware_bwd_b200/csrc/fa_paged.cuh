@@ -713,8 +713,6 @@ __global__ void __launch_bounds__(256) fa_paged_merge_kernel(const __grid_consta
   const int owner = tile_id / p.n_tiles, tile = tile_id % p.n_tiles;
   const PagedRow row = paged_row(p, owner, tile, r);
   if (!row.in_tile) return;
-  const PagedSeq q = paged_seq(p, row.b);
-  if (row.t >= q.row_end) return;
   const bool single = tile >= 2 * p.n_pairs;
   const int S = single ? p.S_single : p.S;
   const long long part = (static_cast<long long>(owner) * p.n_tiles + tile) * p.slots;
@@ -727,6 +725,9 @@ __global__ void __launch_bounds__(256) fa_paged_merge_kernel(const __grid_consta
   for (int s = 0; s < S; ++s) m = fmaxf(m, ml[s * 128].x);
 #pragma unroll 4
   for (int s = 0; s < a.own_S; ++s) m = fmaxf(m, ml2[s].x);
+  // (asked for after the statistics, which do not depend on the lengths)
+  const PagedSeq q = paged_seq(p, row.b);
+  if (row.t >= q.row_end) return;
   float l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   auto add = [&](float2 x, const float4* src) {

@@ -151,8 +151,9 @@ __global__ void __launch_bounds__(kOwnThreads, own_blocks_per_sm(HD)) fa_prefix_
   // first ones are asked for before the length is known).
   const int* row = p.table + static_cast<size_t>(b) * p.max_pages;
   auto entry = [&](int i) {
-    const int page = first_key(i) >> a.log2P;
-    return page < p.max_pages ? __ldg(row + page) : -1;
+    // (unsigned: a group behind the last one may pass 2^31)
+    const uint32_t page = (static_cast<uint32_t>(p.prefix) + 16u * static_cast<uint32_t>(g0 + kw + i * kW)) >> a.log2P;
+    return page < static_cast<uint32_t>(p.max_pages) ? __ldg(row + page) : -1;
   };
   int cur = entry(lane);
 

@@ -273,7 +273,8 @@ fa_status_t fa_decode_paged(const void* q, const void* k_cache, const void* v_ca
  * appends nothing (a bad entry: nothing on that page) and has O = 0, lse =
  * -inf (a bad entry: unspecified).  Table entries behind a sequence's last
  * page are not read, and what the slots behind its last token hold (NaN
- * included) has no influence.
+ * included) has no influence; values of stored tokens are finite (those that
+ * the causal order hides from a row are multiplied by 0, as in fa_fwd).
  */
 
 /*
@@ -307,9 +308,12 @@ fa_status_t fa_append_paged(const void* q, const void* k, const void* v, const i
  * prompt behind a cached prefix, a chunk of a long prompt): new token t of
  * sequence b sees keys 0 .. L - n + t.
  *   q [B][Hq][N][d]  o [B][Hq][N][d] (same dtype)  lse [B][Hq][N] fp32
+ * Hq / Hkv <= 128, otherwise FA_ERR_UNSUPPORTED.
  * workspace (device, 16-byte aligned) of
  * fa_fwd_paged_workspace_bytes(B, Hq, Hkv, N, d, page_size, max_pages) bytes
- * holds partial results; NULL where that is 0.
+ * holds partial results, when few rows meet a long table and the keys are
+ * split over several blocks; NULL where that is 0.  One kernel, or two,
+ * launched as programmatic dependents (see fa_decode_paged).
  */
 size_t fa_fwd_paged_workspace_bytes(int B, int Hq, int Hkv, int N, int d, int page_size,
                                     int max_pages);
@@ -326,8 +330,8 @@ fa_status_t fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache
  * caller sees to it that these pages hold the prefix of every sequence; the
  * entries of the other sequences' tables for it are not read.  A sequence
  * shorter than the prefix sees the part up to its own length.  Limits as
- * fa_decode_paged ((Hq / Hkv) * Nq <= 32).  The cache's prefix slots all hold
- * tokens.
+ * fa_decode_paged ((Hq / Hkv) * Nq <= 32).  The prefix's slots all hold
+ * tokens.  Two kernels, or three, launched as programmatic dependents.
  * workspace (device, 16-byte aligned):
  * fa_decode_prefix_workspace_bytes(B, Hq, Hkv, Nq, d, page_size, max_pages,
  * prefix_len) bytes.

@@ -282,6 +282,93 @@ def test_decode_prefix_peaked_scores(d, P):
     pr.check_attention(o, lse, pr.attention(q, kc, vc, table, lens, [Nq] * 20, 0.5), BF, [Nq] * 20)
 
 
+SPLIT = [
+    # Hq, Hkv, Nq, d, P, prefix, lens, table slack: few sequences with many own
+    # keys (split over several blocks), tables far wider than the sequences
+    (8, 2, 1, 128, 64, 128, (9000, 129, 4000), 1),
+    (4, 1, 2, 64, 16, 0, (7000,), 1),
+    (32, 4, 4, 128, 32, 64, (5000, 70), 3),
+    (8, 2, 1, 128, 16, 16, (17, 20), 3000),
+    (6, 2, 3, 64, 128, 1024, (1027, 1030), 500),
+]
+
+
+@pytest.mark.parametrize("case", SPLIT, ids=lambda c: f"B{len(c[6])}-H{c[0]}/{c[1]}-Nq{c[2]}-d{c[3]}-P{c[4]}-pre{c[5]}")
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp16"])
+def test_own_keys_split_over_blocks(case, dtype):
+    Hq, Hkv, Nq, d, P, prefix, lens, slack = case
+    B = len(lens)
+    kc, vc, table, tl = pr.make_cache(d + P, Hkv, d, P, lens, dtype, prefix=prefix, table_slack=slack)
+    q = torch.randn((B, Hq, Nq, d), generator=torch.Generator().manual_seed(B)).to(dtype)
+    dev = [t.to(DEV) for t in (q, kc, vc, table, tl)]
+    ref = pr.attention(q, kc, vc, table, lens, [Nq] * B, pr.default_scale(d))
+    pr.check_attention(*binding.attention_decode_prefix(*dev, prefix), ref, dtype, [Nq] * B)
+    pr.check_attention(*binding.attention_fwd_paged(*dev), ref, dtype, [Nq] * B)
+    ok()
+
+
+def test_many_heads_to_a_kv_head():
+    """128 query heads share one kv head: a token fills a row tile."""
+    Hq, N, d, P, lens = 128, 3, 64, 16, (200, 3)
+    kc, vc, table, tl = pr.make_cache(2, 1, d, P, lens, BF)
+    q = torch.randn((2, Hq, N, d), generator=torch.Generator().manual_seed(1)).to(BF)
+    o, lse = binding.attention_fwd_paged(*[t.to(DEV) for t in (q, kc, vc, table, tl)])
+    ok()
+    pr.check_attention(o, lse, pr.attention(q, kc, vc, table, lens, [N, N], pr.default_scale(d)), BF, [N, N])
+
+
+def test_no_new_tokens_write_nothing():
+    kc, vc, table, tl = pr.make_cache(2, 2, 64, 16, (40, 20), BF)
+    dev = [t.to(DEV) for t in (kc, vc, table, tl)]
+    x = torch.randn((2, 2, 5, 64)).to(BF).to(DEV)
+    none = torch.zeros(2, dtype=torch.int32, device=DEV)
+    o, lse = torch.full_like(x, 7.0), torch.full((2, 2, 5), 7.0, device=DEV)
+    ws = torch.empty(max(16, binding.fa_fwd_paged_workspace_bytes(2, 2, 2, 5, 64, 16, table.shape[1])), dtype=torch.uint8,
+                     device=DEV)
+    binding.fa_fwd_paged(x, *dev, none, o, lse, 0.125, ws)
+    kd, vd = dev[0].clone(), dev[1].clone()
+    binding.fa_append_paged(x, x, x, o, None, kd, vd, dev[2], dev[3], none, None)
+    ok()
+    assert bool((o == 7).all()) and bool((lse == 7).all())
+    assert torch.equal(kd.view(torch.int16), dev[0].view(torch.int16))
+    assert torch.equal(vd.view(torch.int16), dev[1].view(torch.int16))
+
+
+def test_a_pool_of_more_than_2_32_values():
+    """Pages whose element offset passes 32 bits, written and read back."""
+    Hkv, d, P, dtype, N = 8, 128, 128, BF, 40
+    pages = (1 << 32) // (Hkv * d * P) + 40
+    kc = torch.empty((pages, Hkv, P, d), dtype=dtype, device=DEV)
+    vc = torch.empty_like(kc)
+    lens, prefix = (170, 300), 128
+    table = torch.tensor([[pages - 1, pages - 3, -1], [pages - 1, pages - 2, pages - 5]], dtype=torch.int32)
+    g = torch.Generator().manual_seed(3)
+    small_k, small_v = (torch.randn((6, Hkv, P, d), generator=g).to(dtype) for _ in range(2))
+    local = torch.where(table < 0, table, pages - table)     # the same pages in a small pool
+    for i in (1, 2, 3, 5):
+        kc[pages - i], vc[pages - i] = small_k[i].to(DEV), small_v[i].to(DEV)
+    q, k, v = (torch.randn((2, h, N, d), generator=g).to(dtype) for h in (16, Hkv, Hkv))
+    tl = torch.tensor(lens, dtype=torch.int32)
+    freq = pr.inv_freq(d)
+    args = [t.to(DEV) for t in (table, tl)]
+    q_rot = binding.cache_append(q.to(DEV), k.to(DEV), v.to(DEV), kc, vc, *args, freq.to(DEV))
+    o, lse = binding.attention_fwd_paged(q_rot, kc, vc, *args)
+    one = q_rot[:, :, -1:].contiguous()
+    o1, lse1 = binding.attention_decode_prefix(one, kc, vc, *args, prefix)
+    ok()
+    for i in (1, 2, 3, 5):
+        small_k[i], small_v[i] = kc[pages - i].cpu(), vc[pages - i].cpu()
+    for b, L in enumerate(lens):
+        pos = torch.arange(L - N, L)
+        want, mag = pr.rotated(k[b], pos, freq, False)
+        pr.check_rotated(small_k[local[b].long()[pos // P], :, pos % P].transpose(0, 1).contiguous(), want, mag, "k")
+        assert torch.equal(small_v[local[b].long()[pos // P], :, pos % P].transpose(0, 1), v[b])
+    qc = q_rot.cpu()
+    pr.check_attention(o, lse, pr.attention(qc, small_k, small_v, local, lens, [N, N], pr.default_scale(d)), dtype, [N, N])
+    ref = pr.attention(qc[:, :, -1:].contiguous(), small_k, small_v, local, lens, [1, 1], pr.default_scale(d))
+    pr.check_attention(o1, lse1, ref, dtype, [1, 1])
+
+
 # ------------------------------------------------------------------ bad inputs
 
 @pytest.mark.parametrize("bad", ["page", "page_negative", "too_long", "new_too_many", "new_negative", "short"])
