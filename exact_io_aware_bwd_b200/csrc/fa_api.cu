@@ -786,7 +786,7 @@ struct PagedPlan {
   int64_t owners;   // kv heads, of every sequence in the forward pass
   int S, S_single;  // key splits of a pair of row tiles / of an odd last one
   bool joined;      // partial results go through the workspace
-  int slots() const { return std::max(S, S_single); }
+  int slots() const { return std::max(n_pairs ? S : 0, n_tiles > 2 * n_pairs ? S_single : 0); }
   int64_t rows() const { return owners * n_tiles * 128; }
   size_t o_bytes(int d) const { return joined ? static_cast<size_t>(rows()) * slots() * d * 4u : 0; }
   size_t bytes(int d) const { return joined ? o_bytes(d) + static_cast<size_t>(rows()) * slots() * 8u : 0; }
@@ -794,10 +794,9 @@ struct PagedPlan {
 
 // Splits by a model of the time, in steps of one row tile on one key tile
 // (1 us, half of a pair's): a block costs its steps and 5 more for its start
-// and end; blocks run in waves of one per SM; joining costs 5
-// steps for the launch and the partial results' way through L2 (a row of a
-// split: 8 d + 16 bytes at 5 TB/s).  Up to a wave of splits, at least 2 key
-// tiles each.
+// and end; blocks run in waves of one per SM; joining costs 5 steps for the
+// launch and the partial results' way through L2 (a row of a split: 8 d + 16
+// bytes at 5 TB/s).  Up to a wave of splits, at least 2 key tiles each.
 PagedPlan paged_plan(int B, int Hq, int Hkv, int N, int d, int64_t keys, bool prefix) {
   PagedPlan pl;
   const int G = Hq / Hkv;
@@ -812,27 +811,31 @@ PagedPlan paged_plan(int B, int Hq, int Hkv, int N, int d, int64_t keys, bool pr
   }
   const int64_t tiles = std::max<int64_t>(1, (keys + 127) / 128);
   const int64_t cap = std::min<int64_t>(fa::kDecodeSMs, std::max<int64_t>(1, tiles / 2));
-  // row tiles one by one while even so they do not fill the GPU (a pair reads
-  // each key once for both)
-  const int64_t pairs = pl.owners * pl.n_tiles > fa::kDecodeSMs ? pl.n_tiles / 2 : 0, odd = pl.n_tiles - 2 * pairs;
-  double best = 1e300;
-  pl.n_pairs = static_cast<int>(pairs);
+  pl.n_pairs = 0;
   pl.S = pl.S_single = 1;
-  for (int64_t S = 1; S <= cap; ++S) {
-    const int64_t Ss = odd ? (pairs ? (S + 1) / 2 : S) : 1;
-    const int64_t blocks = pl.owners * (pairs * S + odd * Ss);
-    const double waves = static_cast<double>(blocks) / fa::kDecodeSMs;
-    const double steps = std::max(pairs ? 2.0 * ((tiles + S - 1) / S) : 0.0, odd ? 1.0 * ((tiles + Ss - 1) / Ss) : 0.0);
-    double cost = (waves <= 4 ? std::ceil(waves) : waves) * (steps + 5);
-    if (S > 1 || prefix) cost += 5 + static_cast<double>(pl.rows()) * S * (8.0 * d + 16) / 5e12 / 1e-6;
-    if (cost < best) {
-      best = cost;
-      pl.S = static_cast<int>(S);
-      pl.S_single = static_cast<int>(Ss);
+  double best = 1e300;
+  // Pairs read each key once for two row tiles; row tiles one by one, as many
+  // blocks again, only where that is a tenth faster.
+  for (const int64_t pairs : {static_cast<int64_t>(pl.n_tiles / 2), static_cast<int64_t>(0)}) {
+    const int64_t odd = pl.n_tiles - 2 * pairs;
+    for (int64_t S = 1; S <= cap; ++S) {
+      const int64_t Ss = odd ? (pairs ? (S + 1) / 2 : S) : 1;
+      const int64_t blocks = pl.owners * (pairs * S + odd * Ss);
+      if (S > 1 && blocks > 8 * fa::kDecodeSMs) break;  // the GPU is full
+      const double waves = static_cast<double>(blocks) / fa::kDecodeSMs;
+      const double steps = std::max(pairs ? 2.0 * ((tiles + S - 1) / S) : 0.0, odd ? 1.0 * ((tiles + Ss - 1) / Ss) : 0.0);
+      double cost = (waves <= 4 ? std::ceil(waves) : waves) * (steps + 5);
+      if (S > 1 || prefix) cost += 5 + static_cast<double>(pl.rows()) * S * (8.0 * d + 16) / 5e12 / 1e-6;
+      if (!pairs && pl.n_tiles > 1) cost *= 1.1;
+      if (cost < best) {
+        best = cost;
+        pl.n_pairs = static_cast<int>(pairs);
+        pl.S = static_cast<int>(pairs ? S : Ss);
+        pl.S_single = static_cast<int>(odd ? Ss : S);
+      }
     }
-    if (blocks > 8 * fa::kDecodeSMs) break;  // the GPU is full
+    if (pl.n_tiles < 2 || pl.owners * pl.n_tiles > fa::kDecodeSMs) break;
   }
-  if (!pairs) pl.S = pl.S_single;
   pl.joined = prefix || pl.slots() > 1;
   return pl;
 }
