@@ -802,7 +802,8 @@ PagedPlan paged_plan(int B, int Hq, int Hkv, int N, int d, int64_t keys, bool pr
   const int G = Hq / Hkv;
   pl.toks = prefix ? N : std::min(N, 128 / G);
   pl.seqs = prefix ? std::min(B, 128 / (G * N)) : 1;
-  pl.n_tiles = prefix ? (B + pl.seqs - 1) / pl.seqs : (N + pl.toks - 1) / pl.toks;
+  pl.n_tiles = static_cast<int>(prefix ? (static_cast<int64_t>(B) + pl.seqs - 1) / pl.seqs
+                                       : (static_cast<int64_t>(N) + pl.toks - 1) / pl.toks);
   pl.owners = prefix ? Hkv : static_cast<int64_t>(B) * Hkv;
   if (prefix && keys == 0) {  // nothing shared: no blocks, no partial results
     pl.n_pairs = pl.S = pl.S_single = 0;
@@ -925,7 +926,8 @@ fa_status_t paged_run(const PagedArgs& a, const PagedPlan& pl, void* workspace, 
   prm.S_single = pl.S_single;
   prm.slots = pl.slots();
   prm.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
-  const int64_t blocks = pl.owners * (static_cast<int64_t>(pl.n_pairs) * pl.S + static_cast<int64_t>(pl.n_tiles - 2 * pl.n_pairs) * pl.S_single);
+  const int64_t singles = pl.n_tiles - 2 * static_cast<int64_t>(pl.n_pairs);
+  const int64_t blocks = pl.owners * (static_cast<int64_t>(pl.n_pairs) * pl.S + singles * pl.S_single);
   if (blocks > INT32_MAX) return FA_ERR_UNSUPPORTED;
   auto run = [&](auto kern, auto own1, auto own2, auto merge, int smem) -> fa_status_t {
     fa_status_t r = opt_in_smem(kern, smem);
@@ -951,7 +953,8 @@ fa_status_t paged_run(const PagedArgs& a, const PagedPlan& pl, void* workspace, 
       op.v_cache = a.v_cache;
       // rings as deep as the blocks that share an SM allow
       const int slots = op.S == 1 ? pl.slots() : 0;
-      const int per_sm = static_cast<int>(std::min<int64_t>(fa::own_blocks_per_sm(d), (items + fa::kDecodeSMs - 1) / fa::kDecodeSMs));
+      const int per_sm = static_cast<int>(
+          std::min<int64_t>(fa::own_blocks_per_sm(d), (items + fa::kDecodeSMs - 1) / fa::kDecodeSMs));
       op.stages = fa::kOwnMaxStages;
       while (op.stages > 2 && (fa::own_smem(d, op.stages, G * a.N, slots) + 1024) * per_sm > 228 * 1024) --op.stages;
       const int own_smem = fa::own_smem(d, op.stages, G * a.N, slots);
@@ -1056,7 +1059,8 @@ fa_status_t fa_append_paged(const void* q, const void* k, const void* v, const i
   const bool bf = dtype == FA_BF16;
   auto kern = bf ? (interleaved ? fa::fa_append_kernel<true, true> : fa::fa_append_kernel<true, false>)
                  : (interleaved ? fa::fa_append_kernel<false, true> : fa::fa_append_kernel<false, false>);
-  return launch_dependent(kern, dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), fa::kAppendThreads, 0, st, prm) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy));
+  return launch_dependent(kern, grid, fa::kAppendThreads, 0, st, prm) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 size_t fa_fwd_paged_workspace_bytes(int B, int Hq, int Hkv, int N, int d, int page_size, int max_pages) {

@@ -77,7 +77,7 @@ struct PagedParams {
   int n_tiles;          // row tiles of an owner (kv head, of a sequence in the forward pass)
   int n_pairs;          // the first 2 n_pairs of them in pairs, the others as singles
   int S, S_single;      // key splits of a pair / of a single
-  int slots;            // the larger of the two
+  int slots;            // the larger of those in use
   float scale_log2;
 };
 
@@ -396,9 +396,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_paged_kernel(const __grid_c
       // S_0 S_1 | P_0 V, S_2 | P_1 V, S_3 | ... (two ahead; three at d = 64).
       // S overwrites the tensor memory that the O += P V before it reads P
       // from; the tensor core runs one thread's MMAs in issue order, so no wait
-      // is put between them.  (One
-      // copy of each in the code: a cold instruction line costs microseconds
-      // while every block's first loads are in flight.)
+      // is put between them.  (One copy of each in the code: a cold instruction
+      // line costs microseconds while every block's first loads are in flight.)
       for (int i = 0; ok && i < steps + kDepth; ++i) {
         if (i >= kDepth) ok = issue_pv(i - kDepth);
         if (ok && i < steps) ok = issue_s(i);
@@ -696,10 +695,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_paged_kernel(const __grid_c
 }
 
 // Joins the partial results of every row: those of the key splits above and,
-// behind a shared prefix, those of the sequence's own keys (own_o [row][own_S]
-// [d], own_ml, as the decode kernel leaves them).  A block takes 1024 / d
-// consecutive rows of a row tile: thread = (row, 4 features), rows fastest, so that a warp reads 128 bytes of each split's [d / 4][128] block
-// and 64 of each own row.
+// behind a shared prefix, those of the splits of the sequence's own keys
+// (own_o [row][own_S][d], own_ml [row][own_S]).  A block takes 1024 / d
+// consecutive rows of a row tile: thread = (row, 4 features), rows fastest, so
+// that a warp reads 128 bytes of each split's [d / 4][128] block and 64 of each
+// own row.
 struct PagedMergeParams {
   PagedParams p;
   const float* own_o;   // nullptr: none

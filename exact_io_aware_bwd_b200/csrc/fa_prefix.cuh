@@ -11,9 +11,9 @@
 // tiles, and a stage 32 of its instructions at d = 128.  The stages are filled
 // by 16-byte asynchronous copies of all lanes (as TMA boxes of 16 rows x 128
 // bytes, four a stage, they measured the same, near what an SM's TMA engine
-// takes: some 40 ns a box).  (tcgen05 takes 128 rows or keys at a time and its result through tensor
-// memory: the decode kernel built on it needs about 4 us for a sequence of 150
-// keys however few its rows are.)
+// takes: some 40 ns a box).  (tcgen05 takes 128 rows or keys at a time and its
+// result through tensor memory: the decode kernel built on it needs about 4 us
+// for a sequence of 150 keys however few its rows are.)
 // A warp's time is its instructions (two or three warps share a scheduler), so
 // a stage is kept to about 150 of them: fragments by ldmatrix from 128-byte
 // swizzled rows, a reference max that moves only when a score exceeds it by
