@@ -442,15 +442,6 @@ def _launch(fn, where, dev, stream, args):
         raise FaError(st, where)
 
 
-def _row_strides(where, name, t):
-    """(batch, head, token) strides of a [B, H, N, d] tensor whose rows are
-    contiguous; a dimension of one entry or none is never stepped over."""
-    (b, h, n, d), (sb, sh, sn, sd) = t.shape, t.stride()
-    if sd != 1 and d > 1:
-        raise ValueError(f"{where}: the rows of {name} must be contiguous")
-    return sb if b > 1 else 0, sh if h > 1 else 0, sn if n > 1 else 0
-
-
 _NineStrides = ctypes.c_int64 * 9
 
 
@@ -501,8 +492,11 @@ def fa_append_paged(q, k, v, q_out, k_out, k_cache, v_cache, block_table, seq_le
         _refuse_append(where, q, k, v, q_out, k_out, k_cache, v_cache, block_table, seq_lens, new_lens, inv_freq)
     strides = None
     if not dense:
-        strides = _NineStrides(*((0, 0, 0) if q is None else _row_strides(where, "q", q)), *_row_strides(where, "k", k),
-                               *_row_strides(where, "v", v))
+        ks, vs = k.stride(), v.stride()
+        qs = ks if q is None else q.stride()
+        if (qs[3] != 1 or ks[3] != 1 or vs[3] != 1) and d > 1:
+            raise ValueError(f"{where}: the rows of {'q' if qs[3] != 1 else 'k' if ks[3] != 1 else 'v'} must be contiguous")
+        strides = _NineStrides(qs[0], qs[1], qs[2], ks[0], ks[1], ks[2], vs[0], vs[1], vs[2])
     _launch((_lib or load()).fa_append_paged, where, dev, stream,
             (None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(), strides,
              None if q is None else q_out.data_ptr(), None if k_out is None else k_out.data_ptr(), k_cache.data_ptr(),
@@ -527,9 +521,10 @@ def _refuse_append(where, q, k, v, q_out, k_out, k_cache, v_cache, block_table, 
             raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
         if t is not None and t.dtype is not dt:
             raise TypeError(f"{where}: {name} has dtype {t.dtype}, expected {dt}")
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        if t is not None:
-            _row_strides(where, name, t)
+        if t is not None and t.stride(3) != 1:
+            raise ValueError(f"{where}: the rows of {name} must be contiguous")
+    if k.stride(3) != 1:
+        raise ValueError(f"{where}: the rows of k must be contiguous")
     if inv_freq is not None and (not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1):
         raise ValueError(f"{where}: inv_freq must be a 1-D tensor")
     num_pages, Hc, P, _ = k_cache.shape

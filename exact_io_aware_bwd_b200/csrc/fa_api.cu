@@ -1008,9 +1008,10 @@ fa_status_t fa_append_paged(const void* q, const void* k, const void* v, const i
   for (int i = 0; i < 3; ++i) {
     const int64_t heads = i == 0 ? Hq : Hkv;
     const int64_t dense[3] = {heads * N * d, static_cast<int64_t>(N) * d, d};
+    const int64_t extent[3] = {B, heads, N};  // a dimension of one entry is never stepped over
     long long* dst = i == 0 ? prm.qs : i == 1 ? prm.ks : prm.vs;
     for (int j = 0; j < 3; ++j) {
-      dst[j] = strides ? strides[3 * i + j] : dense[j];
+      dst[j] = extent[j] == 1 ? 0 : strides ? strides[3 * i + j] : dense[j];
       if (dst[j] % 8 != 0 && (i > 0 || q)) return FA_ERR_MISALIGNED;  // rows start on 16-byte boundaries
     }
   }

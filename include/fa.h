@@ -290,7 +290,8 @@ fa_status_t fa_decode_paged(const void* q, const void* k_cache, const void* v_ca
  *   as a dense tensor (the k of fa_fwd for a prompt without cached tokens)
  *   strides: 9 values in host memory, the batch, head and token strides of q,
  *   k and v in elements (NULL: dense), multiples of 8 (a row of d features is
- *   contiguous): rows of a packed projection need no copy.
+ *   contiguous; the stride of a dimension of one entry does not matter): rows
+ *   of a packed projection need no copy.
  * q_out may be q and k_out may be k where those are dense; apart from that no
  * output overlaps another tensor of the call, and no two new tokens share a
  * slot.  One kernel, launched as a programmatic dependent (see

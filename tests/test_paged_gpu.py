@@ -138,6 +138,26 @@ def test_append_in_place_and_without_queries():
         assert torch.equal(got, ref[4])
 
 
+def test_append_from_rows_with_odd_or_zero_strides():
+    """One token a sequence: its token stride is never stepped over, whatever
+    it says; and keys expanded from one head have a head stride of 0."""
+    B, Hq, Hkv, d, P = 3, 4, 2, 64, 16
+    g = torch.Generator().manual_seed(8)
+    flat = torch.randn((B, Hq, d), generator=g).to(BF).to(DEV)
+    q = flat.as_strided((B, Hq, 1, d), (Hq * d, d, 3, 1))
+    k1 = torch.randn((B, 1, 1, d), generator=g).to(BF).to(DEV)
+    k = k1.expand(B, Hkv, 1, d)
+    table = torch.arange(B, dtype=torch.int32, device=DEV)[:, None]
+    lens = torch.tensor([1, 5, 16], dtype=torch.int32, device=DEV)
+    freq = pr.inv_freq(d).to(DEV)
+    caches = [torch.zeros((B, Hkv, P, d), dtype=BF, device=DEV) for _ in range(4)]
+    a = binding.cache_append(q, k, k, caches[0], caches[1], table, lens, freq)
+    b = binding.cache_append(q.contiguous(), k.contiguous(), k.contiguous(), caches[2], caches[3], table, lens, freq)
+    ok()
+    assert torch.equal(a, b) and torch.equal(caches[0], caches[2]) and torch.equal(caches[1], caches[3])
+    assert bool((caches[0].abs().sum((1, 2, 3)) > 0).all())
+
+
 def test_append_far_positions_keep_their_angle():
     """Positions up to the largest a table can hold: the angle is taken in 64
     bits, so a far position is turned as exactly as a near one."""
