@@ -628,7 +628,8 @@ def _allocating(device, stream):
     if stream is None:
         return torch.cuda.stream(torch.cuda.current_stream(device))
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
+        stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream)
+                  else torch.cuda.default_stream(device))
     return torch.cuda.stream(stream)
 
 

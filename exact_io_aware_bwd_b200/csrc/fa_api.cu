@@ -847,8 +847,9 @@ struct PagedArgs {
   void* o;
   float* lse;
   int B, Hq, Hkv, N, d, P, max_pages, num_pages;
-  bool decode;  // behind a prefix (of `prefix` keys)
-  int prefix;
+  bool decode;       // behind a prefix
+  int prefix;        // keys of it that the row-tile pass takes
+  int shared_pages;  // pages of it that the own-key pass takes
   float scale;
   fa_dtype_t dtype;
 };
@@ -862,12 +863,21 @@ int own_splits(int B, int Hkv, int64_t own_keys) {
   return static_cast<int>(std::max<int64_t>(1, std::min((slots + items - 1) / items, own_keys / 1024)));
 }
 
+// Keys of the prefix that get a pass of their own.  A short one is read with
+// the own keys of every sequence instead: one kernel, and while the blocks'
+// reads of it stay few (32/8 heads of 128, prefixes of 128 to 512 keys: 8.5-10.5
+// us with the pass, 5.6-9.7 without, for up to 16 sequences; 1024 keys: 11
+// against 14; 32 sequences: 11.5 against 11.7 at 512 keys).
+int own_pass_prefix(int B, int Hkv, int prefix_len) {
+  return prefix_len <= 512 && static_cast<int64_t>(B) * Hkv * prefix_len <= 65536 ? 0 : prefix_len;
+}
+
 size_t own_bytes(int B, int Hq, int N, int d, int S) {
   return S > 1 ? static_cast<size_t>(B) * Hq * N * S * (static_cast<size_t>(d) + 2) * 4u : 0;
 }
 
-// The paged kernel, where there are keys for it (a forward pass, a prefix);
-// behind a prefix the kernel over each sequence's own keys; the merge kernel
+// The paged kernel, where there are keys for it (a forward pass, a long
+// prefix); in decode the kernel over each sequence's own keys; the merge kernel
 // where the results of several blocks are joined (the own-key kernel does that
 // itself for the prefix's when its own keys are not split).
 fa_status_t paged_run(const PagedArgs& a, const PagedPlan& pl, void* workspace, void* stream) {
@@ -881,23 +891,28 @@ fa_status_t paged_run(const PagedArgs& a, const PagedPlan& pl, void* workspace, 
   std::memset(&mp, 0, sizeof(mp));
   fa::PagedParams prm;
   std::memset(&prm, 0, sizeof(prm));
-  auto enc = encode_fn();
-  if (!enc) return FA_ERR_CUDA;
-  const cuuint64_t rb = static_cast<cuuint64_t>(d) * 2;  // bytes of a row
-  const cuuint64_t dims[5] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(G), static_cast<cuuint64_t>(a.N),
-                              static_cast<cuuint64_t>(a.Hkv), static_cast<cuuint64_t>(a.B)};
-  const cuuint64_t strides[4] = {rb * a.N, rb, rb * a.N * G, rb * a.N * a.Hq};
-  const cuuint32_t box[5] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(pl.toks), 1,
-                             static_cast<cuuint32_t>(pl.seqs)};
-  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
-  if (enc(&prm.tm_q, dt, 5, const_cast<void*>(a.q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-    return FA_ERR_CUDA;
-  const uint64_t outer = static_cast<uint64_t>(a.num_pages) * a.Hkv;
-  if (!make_map(&prm.tm_k, a.k_cache, dt, 2, d, a.P, outer, 64, a.P) ||
-      !make_map(&prm.tm_v, a.v_cache, dt, 2, d, a.P, outer, 64, a.P))
-    return FA_ERR_CUDA;
+  const int64_t singles = pl.n_tiles - 2 * static_cast<int64_t>(pl.n_pairs);
+  const int64_t blocks = pl.owners * (static_cast<int64_t>(pl.n_pairs) * pl.S + singles * pl.S_single);
+  if (blocks > INT32_MAX) return FA_ERR_UNSUPPORTED;
+  if (blocks > 0) {
+    auto enc = encode_fn();
+    if (!enc) return FA_ERR_CUDA;
+    const cuuint64_t rb = static_cast<cuuint64_t>(d) * 2;  // bytes of a row
+    const cuuint64_t dims[5] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(G), static_cast<cuuint64_t>(a.N),
+                                static_cast<cuuint64_t>(a.Hkv), static_cast<cuuint64_t>(a.B)};
+    const cuuint64_t strides[4] = {rb * a.N, rb, rb * a.N * G, rb * a.N * a.Hq};
+    const cuuint32_t box[5] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(pl.toks), 1,
+                               static_cast<cuuint32_t>(pl.seqs)};
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    if (enc(&prm.tm_q, dt, 5, const_cast<void*>(a.q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return FA_ERR_CUDA;
+    const uint64_t outer = static_cast<uint64_t>(a.num_pages) * a.Hkv;
+    if (!make_map(&prm.tm_k, a.k_cache, dt, 2, d, a.P, outer, 64, a.P) ||
+        !make_map(&prm.tm_v, a.v_cache, dt, 2, d, a.P, outer, 64, a.P))
+      return FA_ERR_CUDA;
+  }
   prm.table = a.table;
   prm.lens = a.lens;
   prm.new_lens = a.new_lens;
@@ -926,15 +941,13 @@ fa_status_t paged_run(const PagedArgs& a, const PagedPlan& pl, void* workspace, 
   prm.S_single = pl.S_single;
   prm.slots = pl.slots();
   prm.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
-  const int64_t singles = pl.n_tiles - 2 * static_cast<int64_t>(pl.n_pairs);
-  const int64_t blocks = pl.owners * (static_cast<int64_t>(pl.n_pairs) * pl.S + singles * pl.S_single);
-  if (blocks > INT32_MAX) return FA_ERR_UNSUPPORTED;
   auto run = [&](auto kern, auto own1, auto own2, auto merge, int smem) -> fa_status_t {
-    fa_status_t r = opt_in_smem(kern, smem);
-    if (r != FA_OK) return r;
-    if (blocks > 0 && launch_dependent(kern, dim3(static_cast<unsigned>(blocks)), fa::kFwdThreads, smem, st, prm) !=
-                          cudaSuccess)
-      return FA_ERR_CUDA;
+    fa_status_t r = FA_OK;
+    if (blocks > 0) {
+      if ((r = opt_in_smem(kern, smem)) != FA_OK) return r;
+      if (launch_dependent(kern, dim3(static_cast<unsigned>(blocks)), fa::kFwdThreads, smem, st, prm) != cudaSuccess)
+        return FA_ERR_CUDA;
+    }
     if (a.decode) {
       fa::OwnParams op;
       std::memset(&op, 0, sizeof(op));
@@ -947,6 +960,7 @@ fa_status_t paged_run(const PagedArgs& a, const PagedPlan& pl, void* workspace, 
         op.own_ml = op.own_o + static_cast<size_t>(a.B) * a.Hq * a.N * op.S * d;
       }
       op.follows = a.prefix ? 1 : 0;
+      op.shared_pages = a.shared_pages;
       while ((1 << op.log2P) < a.P) ++op.log2P;
       op.q = a.q;
       op.k_cache = a.k_cache;
@@ -1087,7 +1101,7 @@ fa_status_t fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache
       !aligned4(lse) || !aligned4(block_table) || !aligned4(seq_lens) || !aligned4(new_lens))
     return FA_ERR_MISALIGNED;
   return paged_run({q, k_cache, v_cache, block_table, seq_lens, new_lens, o, lse, B, Hq, Hkv, N, d, page_size,
-                    max_pages, num_pages, false, 0, scale, dtype},
+                    max_pages, num_pages, false, 0, 0, scale, dtype},
                    pl, workspace, stream);
 }
 
@@ -1096,8 +1110,9 @@ size_t fa_decode_prefix_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d, i
   if (B <= 0 || Hq <= 0 || Hkv <= 0 || Nq <= 0 || d <= 0 || page_size <= 0 || max_pages <= 0 || prefix_len < 0 ||
       Hq % Hkv != 0 || static_cast<int64_t>(Hq / Hkv) * Nq > fa::kDecodeMaxRows)
     return 0;
-  return paged_plan(B, Hq, Hkv, Nq, d, prefix_len, true).bytes(d) +
-         own_bytes(B, Hq, Nq, d, own_splits(B, Hkv, static_cast<int64_t>(max_pages) * page_size - prefix_len));
+  const int pass = own_pass_prefix(B, Hkv, prefix_len);
+  return paged_plan(B, Hq, Hkv, Nq, d, pass, true).bytes(d) +
+         own_bytes(B, Hq, Nq, d, own_splits(B, Hkv, static_cast<int64_t>(max_pages) * page_size - pass));
 }
 
 fa_status_t fa_decode_prefix(const void* q, const void* k_cache, const void* v_cache, const int* block_table,
@@ -1111,15 +1126,16 @@ fa_status_t fa_decode_prefix(const void* q, const void* k_cache, const void* v_c
   if (static_cast<int64_t>(Hq / Hkv) * Nq > fa::kDecodeMaxRows) return FA_ERR_UNSUPPORTED;
   if (B == 0) return FA_OK;
   if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !o || !lse) return FA_ERR_INVALID_ARG;
-  const PagedPlan pl = paged_plan(B, Hq, Hkv, Nq, d, prefix_len, true);
+  const int pass = own_pass_prefix(B, Hkv, prefix_len);
+  const PagedPlan pl = paged_plan(B, Hq, Hkv, Nq, d, pass, true);
   const size_t need = pl.bytes(d) + own_bytes(B, Hq, Nq, d,
-                                              own_splits(B, Hkv, static_cast<int64_t>(max_pages) * page_size - prefix_len));
+                                              own_splits(B, Hkv, static_cast<int64_t>(max_pages) * page_size - pass));
   if (need > 0 && (!workspace || workspace_bytes < need)) return FA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o) || !aligned16(workspace) ||
       !aligned4(lse) || !aligned4(block_table) || !aligned4(seq_lens))
     return FA_ERR_MISALIGNED;
   return paged_run({q, k_cache, v_cache, block_table, seq_lens, nullptr, o, lse, B, Hq, Hkv, Nq, d, page_size,
-                    max_pages, num_pages, true, prefix_len, scale, dtype},
+                    max_pages, num_pages, true, pass, pass == 0 ? prefix_len / page_size : 0, scale, dtype},
                    pl, workspace, stream);
 }
 

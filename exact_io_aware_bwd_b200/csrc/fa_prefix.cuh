@@ -25,7 +25,8 @@
 // warps and of the prefix's splits meet at the end:
 //   m* = max m_s, l* = sum l_s 2^(m_s - m*), O = sum O_s 2^(m_s - m*) / l*.
 // With few sequences and many own keys these are split over several blocks,
-// and fa_paged_merge_kernel joins them instead.
+// and fa_paged_merge_kernel joins them instead.  A short prefix is taken with
+// the own keys, by every sequence again (from L2): one kernel instead of two.
 //
 // 96 sequences x 8 heads of 500 own keys on average (196 MB): 32-36 us behind
 // the prefix pass, about 6 TB/s; 50 x 12 of 150 keys of 64: 10.6 us, most of it
@@ -58,6 +59,7 @@ struct OwnParams {
   int stages;           // of a warp's ring
   int log2P;            // log2 of the page size
   int follows;          // the prefix kernel precedes this one in the stream
+  int shared_pages;     // pages found through sequence 0's table (a short prefix, taken with the own keys)
 };
 
 // 16 bytes global -> shared, the bytes behind the first `bytes` as zeros.
@@ -158,7 +160,8 @@ __global__ void __launch_bounds__(kOwnThreads, own_blocks_per_sm(HD)) fa_prefix_
   auto entry = [&](int i) {
     // (unsigned: a group behind the last one may pass 2^31)
     const uint32_t page = (static_cast<uint32_t>(p.prefix) + 16u * static_cast<uint32_t>(g0 + kw + i * kW)) >> a.log2P;
-    return page < static_cast<uint32_t>(p.max_pages) ? __ldg(row + page) : -1;
+    const int* from = page < static_cast<uint32_t>(a.shared_pages) ? p.table : row;
+    return page < static_cast<uint32_t>(p.max_pages) ? __ldg(from + page) : -1;
   };
   int cur = entry(lane);
 

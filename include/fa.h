@@ -332,7 +332,9 @@ fa_status_t fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache
  * entries of the other sequences' tables for it are not read.  A sequence
  * shorter than the prefix sees the part up to its own length.  Limits as
  * fa_decode_paged ((Hq / Hkv) * Nq <= 32).  The prefix's slots all hold
- * tokens.  Two kernels, or three, launched as programmatic dependents.
+ * tokens.  A prefix of up to 512 tokens may be read by each sequence instead,
+ * where that is faster.  One to three kernels, launched as programmatic
+ * dependents.
  * workspace (device, 16-byte aligned):
  * fa_decode_prefix_workspace_bytes(B, Hq, Hkv, Nq, d, page_size, max_pages,
  * prefix_len) bytes.

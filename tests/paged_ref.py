@@ -31,6 +31,7 @@ def make_cache(seed, Hkv, d, P, lens, dtype, prefix=0, spare=4, table_slack=1, g
     vc = torch.full((count, Hkv, P, d), garbage).to(dtype)
     table = torch.full((len(lens), width), -1, dtype=torch.int32)
     used = shared
+    first_live = next((b for b, L in enumerate(lens) if L > 0), 0)
     for b, (L, n) in enumerate(zip(lens, own)):
         if L == 0:
             continue
@@ -39,7 +40,7 @@ def make_cache(seed, Hkv, d, P, lens, dtype, prefix=0, spare=4, table_slack=1, g
         used += n
         for i in range(-(-max(L, prefix) // P)):
             page, m = int(table[b, i]), min(P, max(L, prefix) - i * P)
-            if i < shared and b > 0 and lens[0] > 0:
+            if i < shared and b > first_live:
                 continue
             kc[page, :, :m] = torch.randn((Hkv, m, d), generator=g).to(dtype)
             vc[page, :, :m] = torch.randn((Hkv, m, d), generator=g).to(dtype)

@@ -447,6 +447,36 @@ def test_bad_prefix_page_is_reported():
     ok()
 
 
+def test_bad_page_of_a_long_prefix_is_reported():
+    Hq, Hkv, d, P, prefix, lens = 8, 2, 128, 16, 2048, (2100, 2060)
+    kc, vc, table, tl = pr.make_cache(3, Hkv, d, P, lens, BF, prefix=prefix)
+    table[0, 77] = -4
+    q = torch.randn((2, Hq, 1, d)).to(BF).to(DEV)
+    binding.attention_decode_prefix(q, kc.to(DEV), vc.to(DEV), table.to(DEV), tl.to(DEV), prefix)
+    assert binding.fa_get_device_status() == binding.FA_ERR_INVALID_ARG
+    ok()
+
+
+@pytest.mark.parametrize("prefix", [64, 512, 528])
+@pytest.mark.parametrize("B", [2, 17, 70])
+def test_prefix_lengths_around_the_pass_of_their_own(prefix, B):
+    """Short prefixes are taken with the own keys, longer ones and those of
+    many sequences in a pass of their own; sequence 0 idle or not."""
+    Hq, Hkv, Nq, d, P = 8, 4, 2, 128, 16
+    for first in (prefix + 5, 0):
+        lens = (first,) + tuple(prefix + 2 + 7 * i for i in range(B - 1))
+        kc, vc, table, tl = pr.make_cache(B, Hkv, d, P, lens, BF, prefix=prefix)
+        if first == 0:   # the prefix is still found through sequence 0's table
+            table[0, :prefix // P] = table[1, :prefix // P]
+        q = torch.randn((B, Hq, Nq, d), generator=torch.Generator().manual_seed(B)).to(BF)
+        ref = pr.attention(q, kc, vc, table, lens, [Nq] * B, pr.default_scale(d))
+        seen = table.clone()
+        seen[1:, :prefix // P] = -1
+        o, lse = binding.attention_decode_prefix(q.to(DEV), kc.to(DEV), vc.to(DEV), seen.to(DEV), tl.to(DEV), prefix)
+        ok()
+        pr.check_attention(o, lse, ref, BF, [Nq] * B)
+
+
 # ---------------------------------------------------------------- as one server
 
 class Server:
@@ -633,6 +663,19 @@ def test_calls_on_two_streams_do_not_meet():
         for o, lse in outs:
             pr.check_attention(o, lse, ref, FP, [N] * B)
     ok()
+
+
+def test_the_default_stream_by_its_number():
+    kc, vc, table, tl = pr.make_cache(2, 2, 64, 16, (40, 20), BF)
+    q = torch.randn((2, 2, 5, 64), generator=torch.Generator().manual_seed(1)).to(BF)
+    dev = [t.to(DEV) for t in (q, kc, vc, table, tl)]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        o, lse = binding.attention_fwd_paged(*dev, stream=0)
+    torch.cuda.synchronize()
+    ok()
+    pr.check_attention(o, lse, pr.attention(q, kc, vc, table, (40, 20), (5, 5), pr.default_scale(64)), BF, (5, 5))
 
 
 def test_results_repeat_bit_for_bit():
