@@ -385,6 +385,7 @@ def fa_decode_paged(q, k_cache, v_cache, block_table, seq_lens, o, lse, scale: f
 # microseconds: plain comparisons, one pass over the tensors.
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _fits(where, dev, *spec):
@@ -426,18 +427,21 @@ def _table_width(where, block_table):
     return block_table.shape[1]
 
 
-def _launch(fn, where, dev, stream, args):
-    """fn(*args, stream) with `dev` current; the default stream is the
-    current one of that device, whichever device is current."""
+def _handle(dev, stream):
+    """The stream of a call: the current one of the tensors' device, whichever
+    device is current, when none is given."""
     if stream is None:
-        stream = _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
-    elif isinstance(stream, torch.cuda.Stream):
-        stream = stream.cuda_stream
-    if dev == torch.cuda.current_device():
-        st = fn(*args, stream)
+        return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _launch(fn, where, dev, *args):
+    """fn(*args) with device `dev` current."""
+    if dev == _current_device():
+        st = fn(*args)
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, stream)
+            st = fn(*args)
     if st != FA_OK:
         raise FaError(st, where)
 
@@ -497,12 +501,12 @@ def fa_append_paged(q, k, v, q_out, k_out, k_cache, v_cache, block_table, seq_le
         if (qs[3] != 1 or ks[3] != 1 or vs[3] != 1) and d > 1:
             raise ValueError(f"{where}: the rows of {'q' if qs[3] != 1 else 'k' if ks[3] != 1 else 'v'} must be contiguous")
         strides = _NineStrides(qs[0], qs[1], qs[2], ks[0], ks[1], ks[2], vs[0], vs[1], vs[2])
-    _launch((_lib or load()).fa_append_paged, where, dev, stream,
-            (None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(), strides,
-             None if q is None else q_out.data_ptr(), None if k_out is None else k_out.data_ptr(), k_cache.data_ptr(),
-             v_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
-             None if new_lens is None else new_lens.data_ptr(), None if inv_freq is None else inv_freq.data_ptr(),
-             B, Hq, Hkv, N, d, P, max_pages, num_pages, rot, 1 if interleaved else 0, dtype_code))
+    _launch((_lib or load()).fa_append_paged, where, dev,
+            None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(), strides,
+            None if q is None else q_out.data_ptr(), None if k_out is None else k_out.data_ptr(), k_cache.data_ptr(),
+            v_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+            None if new_lens is None else new_lens.data_ptr(), None if inv_freq is None else inv_freq.data_ptr(),
+            B, Hq, Hkv, N, d, P, max_pages, num_pages, rot, 1 if interleaved else 0, dtype_code, _handle(dev, stream))
 
 
 def _refuse_append(where, q, k, v, q_out, k_out, k_cache, v_cache, block_table, seq_lens, new_lens, inv_freq):
@@ -599,8 +603,8 @@ def fa_fwd_paged(q, k_cache, v_cache, block_table, seq_lens, new_lens, o, lse, s
     where = "fa_fwd_paged"
     dev, ins, outs, sizes, dt, ws = _attention_paged(where, q, k_cache, v_cache, block_table, seq_lens, new_lens, o, lse,
                                                      workspace)
-    _launch((_lib or load()).fa_fwd_paged, where, dev, stream,
-            (*ins, None if new_lens is None else new_lens.data_ptr(), *outs, *sizes, scale, dt, *ws))
+    _launch((_lib or load()).fa_fwd_paged, where, dev, *ins, None if new_lens is None else new_lens.data_ptr(), *outs,
+            *sizes, scale, dt, *ws, _handle(dev, stream))
 
 
 def fa_decode_prefix_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, d: int, page_size: int, max_pages: int,
@@ -617,7 +621,8 @@ def fa_decode_prefix(q, k_cache, v_cache, block_table, seq_lens, o, lse, scale: 
     where = "fa_decode_prefix"
     dev, ins, outs, sizes, dt, ws = _attention_paged(where, q, k_cache, v_cache, block_table, seq_lens, None, o, lse,
                                                      workspace)
-    _launch((_lib or load()).fa_decode_prefix, where, dev, stream, (*ins, *outs, *sizes, prefix_len, scale, dt, *ws))
+    _launch((_lib or load()).fa_decode_prefix, where, dev, *ins, *outs, *sizes, prefix_len, scale, dt, *ws,
+            _handle(dev, stream))
 
 
 # ------------------------------------------------------------ conveniences
