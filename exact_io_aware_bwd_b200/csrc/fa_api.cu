@@ -815,8 +815,11 @@ PagedPlan paged_plan(int B, int Hq, int Hkv, int N, int d, int64_t keys, bool pr
   pl.n_pairs = 0;
   pl.S = pl.S_single = 1;
   double best = 1e300;
-  // Pairs read each key once for two row tiles; row tiles one by one, as many
-  // blocks again, only where that is a tenth faster.
+  // Pairs read each key once for two row tiles.  While row tiles one by one do
+  // not fill the GPU either, those: an odd number of them always (3 tiles x 8
+  // heads on 65 536 keys: 161 us against 167 with a pair and an odd one), an
+  // even number where that is modelled a tenth faster (2 tiles x 32 on 16 000
+  // keys, modelled alike: 76.7 us against 74.8 in pairs).
   for (const int64_t pairs : {static_cast<int64_t>(pl.n_tiles / 2), static_cast<int64_t>(0)}) {
     const int64_t odd = pl.n_tiles - 2 * pairs;
     for (int64_t S = 1; S <= cap; ++S) {
@@ -827,7 +830,7 @@ PagedPlan paged_plan(int B, int Hq, int Hkv, int N, int d, int64_t keys, bool pr
       const double steps = std::max(pairs ? 2.0 * ((tiles + S - 1) / S) : 0.0, odd ? 1.0 * ((tiles + Ss - 1) / Ss) : 0.0);
       double cost = (waves <= 4 ? std::ceil(waves) : waves) * (steps + 5);
       if (S > 1 || prefix) cost += 5 + static_cast<double>(pl.rows()) * S * (8.0 * d + 16) / 5e12 / 1e-6;
-      if (!pairs && pl.n_tiles > 1) cost *= 1.1;
+      if (!pairs) cost *= pl.n_tiles % 2 ? 0.99 : 1.1;
       if (cost < best) {
         best = cost;
         pl.n_pairs = static_cast<int>(pairs);
