@@ -962,7 +962,6 @@ fa_status_t paged_run(const PagedArgs& a, const PagedPlan& pl, void* workspace, 
         op.own_o = reinterpret_cast<float*>(ws + pl.bytes(d));
         op.own_ml = op.own_o + static_cast<size_t>(a.B) * a.Hq * a.N * op.S * d;
       }
-      op.follows = a.prefix ? 1 : 0;
       op.shared_pages = a.shared_pages;
       while ((1 << op.log2P) < a.P) ++op.log2P;
       op.q = a.q;

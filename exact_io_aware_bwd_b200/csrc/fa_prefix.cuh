@@ -28,10 +28,9 @@
 // and fa_paged_merge_kernel joins them instead.  A short prefix is taken with
 // the own keys, by every sequence again (from L2): one kernel instead of two.
 //
-// 96 sequences x 8 heads of 500 own keys on average (196 MB): 32-36 us behind
-// the prefix pass, about 6 TB/s; 50 x 12 of 150 keys of 64: 10.6 us, most of it
-// the wait for the prefix kernel's end (1.6 us), the join (3 us) and the first
-// loads.
+// 96 sequences x 8 heads of 500 own keys on average (196 MB): 40-42 us behind
+// the prefix pass, 4.8 TB/s; 50 x 12 of 150 keys of 64: 13.4 us, most of it
+// the first loads behind the prefix kernel's end and the join (3 us).
 #pragma once
 
 #include "fa_paged.cuh"
@@ -58,7 +57,6 @@ struct OwnParams {
   int S;
   int stages;           // of a warp's ring
   int log2P;            // log2 of the page size
-  int follows;          // the prefix kernel precedes this one in the stream
   int shared_pages;     // pages found through sequence 0's table (a short prefix, taken with the own keys)
 };
 
@@ -138,10 +136,10 @@ __global__ void __launch_bounds__(kOwnThreads, own_blocks_per_sm(HD)) fa_prefix_
   }
   __syncwarp();
 
-  // The inputs were written before the prefix kernel started (it waits for
-  // them before it lets this kernel be scheduled); only its results are
-  // waited for, at the end.
-  if (!a.follows) grid_dependency_wait();
+  // Before anything is read, the inputs included: those of a step come from the
+  // append in front of the prefix kernel, and that an earlier kernel's writes
+  // are visible is promised only to a kernel that has waited.
+  grid_dependency_wait();
   grid_launch_dependents();
 
   const int L = p.lens[b];
@@ -333,7 +331,6 @@ __global__ void __launch_bounds__(kOwnThreads, own_blocks_per_sm(HD)) fa_prefix_
         *reinterpret_cast<float2*>(sO + r * HD + 8 * j + 2 * qd) = make_float2(o[j][2 * e], o[j][2 * e + 1]);
   }
   const bool last = a.S == 1;
-  if (last && a.follows) grid_dependency_wait();  // the prefix's partial results
   __syncthreads();
   // Weights of a row's partial results: a warp takes rows in turn, its lanes
   // the prefix's splits.
@@ -399,9 +396,6 @@ __global__ void __launch_bounds__(kOwnThreads, own_blocks_per_sm(HD)) fa_prefix_
       reinterpret_cast<float4*>(a.own_o + ((out0 + r) * a.S + split) * HD)[c4] = acc;
     }
   }
-  // the prefix kernel, too, is complete before this one is: whoever waits for
-  // this kernel may read what both left
-  if (a.S > 1 && a.follows) grid_dependency_wait();
 }
 
 }  // namespace fa

@@ -334,7 +334,7 @@ fa_status_t fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache
  * fa_decode_paged ((Hq / Hkv) * Nq <= 32).  The prefix's slots all hold
  * tokens.  A prefix of up to 512 tokens may be read by each sequence instead,
  * where that is faster.  One to three kernels, launched as programmatic
- * dependents.
+ * dependents (see fa_decode_paged).
  * workspace (device, 16-byte aligned):
  * fa_decode_prefix_workspace_bytes(B, Hq, Hkv, Nq, d, page_size, max_pages,
  * prefix_len) bytes.

@@ -1,0 +1,48 @@
+"""What can be seen of the paged-cache kernels without a GPU: that each kernel
+launched as a programmatic dependent (scheduled while the kernel before it still
+runs) waits for that kernel before it touches global memory."""
+
+import os
+import re
+
+import pytest
+
+from exact_io_aware_bwd_b200.build import CSRC
+
+KERNELS = [("fa_append.cuh", "fa_append_kernel"), ("fa_paged.cuh", "fa_paged_kernel"),
+           ("fa_paged.cuh", "fa_paged_merge_kernel"), ("fa_prefix.cuh", "fa_prefix_own_kernel")]
+# the first thing a kernel may do with global memory, as these kernels write it
+TOUCHES = re.compile(r"\bp\.(lens|table|new_lens|part_ml|inv_freq|o|lse)\b|paged_seq\(|paged_item_keys\(|tma_load_|"
+                     r"copy16_async\(|__ldg\(|\ba\.(q|own_ml|own_o|k_cache|v_cache)\b")
+
+
+def source(name):
+    with open(os.path.join(CSRC, name)) as f:
+        return re.sub(r"//[^\n]*", "", f.read())
+
+
+def body(text, kernel):
+    start = text.index("{", re.search(rf"__global__[^;{{]*\b{kernel}\(", text).end())
+    depth = 0
+    for i in range(start, len(text)):
+        depth += {"{": 1, "}": -1}.get(text[i], 0)
+        if depth == 0:
+            return text[start:i]
+    raise AssertionError(kernel)
+
+
+@pytest.mark.parametrize("file,kernel", KERNELS, ids=[k for _, k in KERNELS])
+def test_waits_before_it_touches_global_memory(file, kernel):
+    code = body(source(file), kernel)
+    wait = re.search(r"^  grid_dependency_wait\(\);", code, re.M)  # a statement of the body itself: under no condition
+    assert wait, "no unconditional wait"
+    touch = TOUCHES.search(code)
+    assert touch and wait.start() < touch.start(), f"{touch.group()} comes before the wait"
+
+
+def test_every_dependent_launch_of_the_paged_calls_is_listed():
+    text = source("fa_api.cu")
+    part = text[text.index("fa_status_t check_paged("):]
+    launched = set(re.findall(r"fa::(fa_\w+_kernel)<", part))
+    assert {k for _, k in KERNELS} <= launched | {"fa_append_kernel"}
+    assert not {k for k in launched if k.startswith(("fa_append", "fa_paged", "fa_prefix"))} - {k for _, k in KERNELS}

@@ -1,0 +1,143 @@
+"""Steps of a server whose prefix has a pass of its own: append, prefix pass,
+own keys and (where these are split) the join run one behind the other on
+inputs that change from step to step, eager and captured; a step's kernels on a
+shared workspace and on two streams.  Each test first makes sure that its sizes
+take that path: then, and only then, decode needs a workspace."""
+
+import pytest
+import torch
+
+import paged_ref as pr
+import test_paged_gpu as tp
+from exact_io_aware_bwd_b200 import binding
+from exact_io_aware_bwd_b200.build import build
+
+pytestmark = pytest.mark.gpu
+
+DEV, BF, FP = tp.DEV, tp.BF, tp.FP
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    build()
+    binding.load()
+
+
+def workspace(nbytes):
+    assert nbytes > 0
+    return torch.full((nbytes,), 255, dtype=torch.uint8, device=DEV)
+
+
+def server(dtype, wide, **kw):
+    """Behind a prefix of 1024 keys; wide: with room in the table for so many
+    own keys that these are split, and joined by a third kernel."""
+    s = tp.Server(dtype, prefix=1024, **kw)
+    if wide:
+        s.table = torch.cat([s.table, torch.full((len(s.prompts), 4096 // s.P), -1, dtype=torch.int32)], 1)
+    sizes = lambda pages: (len(s.prompts), s.Hq, s.Hkv, 1, s.d, s.P, pages, s.prefix)
+    narrow = binding.fa_decode_prefix_workspace_bytes(*sizes(s.prefix // s.P + 2))
+    here = binding.fa_decode_prefix_workspace_bytes(*sizes(s.table.shape[1]))
+    assert here > narrow > 0 if wide else here == narrow > 0
+    return s
+
+
+@pytest.mark.parametrize("wide", [False, True], ids=["own_unsplit", "own_split"])
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp16"])
+def test_steps_behind_a_long_prefix(dtype, wide):
+    server(dtype, wide).run()
+
+
+@pytest.mark.parametrize("wide", [False, True], ids=["own_unsplit", "own_split"])
+def test_captured_steps_behind_a_long_prefix(wide):
+    """Append and decode captured as one graph; each step copies its tokens
+    and lengths in and replays it."""
+    state = {}
+
+    def step(s, table, freq, q, k, v, lens):
+        if not state:
+            for n, t in dict(q=q, k=k, v=v, lens=lens).items():
+                state[n] = t.clone()
+            B, Hq, _, d = q.shape
+            o, lse, q_rot = torch.empty_like(q), torch.empty((B, Hq, 1), device=DEV), torch.empty_like(q)
+            ws = workspace(binding.fa_decode_prefix_workspace_bytes(B, Hq, s.Hkv, 1, d, s.P, table.shape[1], s.prefix))
+
+            def work():
+                binding.fa_append_paged(state["q"], state["k"], state["v"], q_rot, None, s.kc, s.vc, table, state["lens"],
+                                        None, freq)
+                binding.fa_decode_prefix(q_rot, s.kc, s.vc, table, state["lens"], o, lse, pr.default_scale(d), s.prefix, ws)
+
+            work()  # outside the capture first: loads the kernels
+            torch.cuda.synchronize()
+            state["graph"] = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(state["graph"]):
+                work()
+            state["out"] = (o, lse, q_rot, ws)
+        for n, t in dict(q=q, k=k, v=v, lens=lens).items():
+            state[n].copy_(t)
+        state["graph"].replay()
+        return state["out"][:2]
+
+    server(BF, wide, steps=8).run(step)
+
+
+@pytest.mark.parametrize("wide", [0, 300], ids=["own_unsplit", "own_split"])
+def test_layers_in_a_row_equal_calls_apart(wide):
+    """Three layers of a step, each layer's queries the output of the one
+    before, all on one workspace: back to back, and replayed as a graph, they
+    give bit for bit what they give with a wait for the GPU after every call."""
+    B, Hq, Hkv, d, P, prefix, layers = 5, 8, 2, 128, 16, 1024, 3
+    lens0 = [prefix + 20 + 9 * b for b in range(B)]
+    g = torch.Generator().manual_seed(2)
+    _, _, table, _ = pr.make_cache(1, Hkv, d, P, [n + 40 for n in lens0], BF, prefix=prefix, table_slack=1 + wide)
+    pages = int(table.max()) + 1
+    table, freq = table.to(DEV), pr.inv_freq(d).to(DEV)
+    scale = pr.default_scale(d)
+    ws = workspace(binding.fa_decode_prefix_workspace_bytes(B, Hq, Hkv, 1, d, P, table.shape[1], prefix))
+    start = [torch.randn((layers, pages, Hkv, P, d), generator=g).to(BF).to(DEV) for _ in range(2)]
+    steps = [[torch.randn((B, h, 1, d), generator=g).to(BF).to(DEV) for h in (Hq, Hkv, Hkv)] for _ in range(10)]
+    lens = [torch.tensor([n + 1 + i for n in lens0], dtype=torch.int32, device=DEV) for i in range(len(steps))]
+
+    def buffers():
+        x = [t.clone() for t in steps[0]] + [lens[0].clone()] + [t.clone() for t in start]
+        return x, torch.empty_like(steps[0][0]), [torch.empty_like(steps[0][0]) for _ in range(layers)], \
+            torch.empty((layers, B, Hq, 1), device=DEV)
+
+    def work(bufs, apart):
+        (q, k, v, n, kc, vc), q_rot, outs, lse = bufs
+        for i in range(layers):
+            binding.fa_append_paged(q if i == 0 else outs[i - 1], k, v, q_rot, None, kc[i], vc[i], table, n, None, freq)
+            if apart:
+                torch.cuda.synchronize()
+            binding.fa_decode_prefix(q_rot, kc[i], vc[i], table, n, outs[i], lse[i], scale, prefix, ws)
+            if apart:
+                torch.cuda.synchronize()
+
+    def all_steps(go):
+        bufs = buffers()
+        results = []
+        for tokens, n in zip(steps, lens):
+            for dst, src in zip(bufs[0], tokens + [n]):
+                dst.copy_(src)
+            go(bufs)
+            results.append(([o.clone() for o in bufs[2]], bufs[3].clone()))
+        torch.cuda.synchronize()
+        return results
+
+    want = all_steps(lambda bufs: work(bufs, True))
+    in_a_row = all_steps(lambda bufs: work(bufs, False))
+    made = {}
+
+    def replayed(bufs):
+        if not made:
+            made["graph"] = torch.cuda.CUDAGraph()
+            torch.cuda.synchronize()
+            with torch.cuda.graph(made["graph"]):
+                work(bufs, False)
+        made["graph"].replay()
+
+    in_a_graph = all_steps(replayed)
+    tp.ok()
+    assert bool(torch.isfinite(want[-1][1]).all())
+    for got in (in_a_row, in_a_graph):
+        for (a, la), (b, lb) in zip(got, want):
+            assert all(torch.equal(x, y) for x, y in zip(a, b)) and torch.equal(la, lb)
