@@ -280,11 +280,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_paged_kernel(const __grid_c
   PagedItem it = paged_item(p);
   const bool single = it.single;
   // unsplit, the first table entries are asked for before the length is known
+  // (all by plain loads: the read-only path is for data that nobody writes
+  // while the kernel is resident, and it is resident before its wait)
   const int* row_table = p.table + static_cast<size_t>(it.b) * p.max_pages;
   int cur = -1, nxt = -1;  // table entries of 32 pages, one a lane, and of the next 32
   if (produces && it.splits == 1) {
-    if (lane < p.max_pages) cur = __ldg(row_table + lane);
-    if (lane + 32 < p.max_pages) nxt = __ldg(row_table + lane + 32);
+    if (lane < p.max_pages) cur = row_table[lane];
+    if (lane + 32 < p.max_pages) nxt = row_table[lane + 32];
   }
   paged_item_keys(p, it);
   if (warp == 11) {
@@ -296,7 +298,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_paged_kernel(const __grid_c
     const int ppt = kPagedTile / p.P;  // pages of a key tile
     if (it.n_kv > 0) {
       const int n_pages = (it.valid_end + p.P - 1) / p.P, pg0 = it.k0 * ppt;
-      auto entry = [&](int rel) { return pg0 + rel < n_pages ? __ldg(row_table + pg0 + rel) : -1; };
+      auto entry = [&](int rel) { return pg0 + rel < n_pages ? row_table[pg0 + rel] : -1; };
       if (it.splits > 1) cur = entry(lane), nxt = entry(32 + lane);
       bool ok = true;
       for (int kt = 0; kt < it.n_kv; ++kt) {

@@ -153,13 +153,14 @@ __global__ void __launch_bounds__(kOwnThreads, own_blocks_per_sm(HD)) fa_prefix_
   const int n_mine = g1 - g0 > kw ? (g1 - g0 - kw + kW - 1) / kW : 0;
   auto first_key = [&](int i) { return p.prefix + 16 * (g0 + kw + i * kW); };
   // Table entries of the warp's groups, 32 at a time, one a lane (unsplit, the
-  // first ones are asked for before the length is known).
+  // first ones are asked for before the length is known; by plain loads, as in
+  // the row-tile kernel).
   const int* row = p.table + static_cast<size_t>(b) * p.max_pages;
   auto entry = [&](int i) {
     // (unsigned: a group behind the last one may pass 2^31)
     const uint32_t page = (static_cast<uint32_t>(p.prefix) + 16u * static_cast<uint32_t>(g0 + kw + i * kW)) >> a.log2P;
     const int* from = page < static_cast<uint32_t>(a.shared_pages) ? p.table : row;
-    return page < static_cast<uint32_t>(p.max_pages) ? __ldg(from + page) : -1;
+    return page < static_cast<uint32_t>(p.max_pages) ? from[page] : -1;
   };
   int cur = entry(lane);
 

@@ -46,3 +46,10 @@ def test_every_dependent_launch_of_the_paged_calls_is_listed():
     launched = set(re.findall(r"fa::(fa_\w+_kernel)<", part))
     assert {k for _, k in KERNELS} <= launched | {"fa_append_kernel"}
     assert not {k for k in launched if k.startswith(("fa_append", "fa_paged", "fa_prefix"))} - {k for _, k in KERNELS}
+
+
+@pytest.mark.parametrize("file,kernel", KERNELS, ids=[k for _, k in KERNELS])
+def test_tables_and_lengths_are_not_read_as_constants(file, kernel):
+    """__ldg (ld.global.nc) asks that nobody writes the data while the kernel
+    is resident; a dependent launch is resident before its inputs are written."""
+    assert "__ldg" not in body(source(file), kernel)
