@@ -615,7 +615,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_paged_kernel(const __grid_c
       m_ref = m;
     }
     if (have || have_other) tc_fence_after();
-    const bool seen = l_sum > 0.f;
+    const bool seen = l_sum != 0.f;  // NaN too: scores that are no numbers show in O and lse
     const bool direct = p.part_o == nullptr;
     if (direct) {
       const float inv_l = seen ? 1.f / l_sum : 0.f;
@@ -737,26 +737,26 @@ __global__ void __launch_bounds__(256) fa_paged_merge_kernel(const __grid_consta
   // (asked for after the statistics, which do not depend on the lengths)
   const PagedSeq q = paged_seq(p, row.b);
   if (row.t >= q.row_end) return;
+  // a maximum of -inf does not say that the row saw nothing: NaN is no maximum
+  const float ref = m == -INFINITY ? 0.f : m;
   float l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   auto add = [&](float2 x, const float4* src) {
-    const float w = ex2_approx(x.x - m);  // 0 for an empty split, whose O is 0
+    const float w = ex2_approx(x.x - ref);  // 0 for an empty split, whose O is 0
     const float4 y = *src;
     l += x.y * w;
     o.x += y.x * w, o.y += y.y * w, o.z += y.z * w, o.w += y.w * w;
   };
-  if (m != -INFINITY) {
 #pragma unroll 4
-    for (int s = 0; s < S; ++s) add(ml[s * 128], po + static_cast<long long>(s) * (HD / 4) * 128);
+  for (int s = 0; s < S; ++s) add(ml[s * 128], po + static_cast<long long>(s) * (HD / 4) * 128);
 #pragma unroll 4
-    for (int s = 0; s < a.own_S; ++s) add(ml2[s], po2 + s * (HD / 4));
-  }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  for (int s = 0; s < a.own_S; ++s) add(ml2[s], po2 + s * (HD / 4));
+  const float inv = l != 0.f ? 1.f / l : 0.f;
   uint2 w;
   w.x = pack2<BF16>(o.x * inv, o.y * inv);
   w.y = pack2<BF16>(o.z * inv, o.w * inv);
   *reinterpret_cast<uint2*>(reinterpret_cast<T*>(p.o) + row.out * HD + 4 * c4) = w;
-  if (c4 == 0) p.lse[row.out] = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+  if (c4 == 0) p.lse[row.out] = l != 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
 }  // namespace fa

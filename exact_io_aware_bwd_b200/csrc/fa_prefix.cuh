@@ -364,9 +364,9 @@ __global__ void __launch_bounds__(kOwnThreads, own_blocks_per_sm(HD)) fa_prefix_
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, x);
     if (lane == 0) {
-      sInv[r] = !last ? 1.f : ls > 0.f ? 1.f / ls : 0.f;
+      sInv[r] = !last ? 1.f : ls != 0.f ? 1.f / ls : 0.f;  // (NaN shows)
       if (last)
-        p.lse[out0 + r] = ls > 0.f ? (ms + __log2f(ls)) * 0.69314718055994531f : -INFINITY;
+        p.lse[out0 + r] = ls != 0.f ? (ms + __log2f(ls)) * 0.69314718055994531f : -INFINITY;
       else
         reinterpret_cast<float2*>(a.own_ml)[(out0 + r) * a.S + split] = make_float2(ms, ls);
     }

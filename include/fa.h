@@ -274,7 +274,10 @@ fa_status_t fa_decode_paged(const void* q, const void* k_cache, const void* v_ca
  * -inf (a bad entry: unspecified).  Table entries behind a sequence's last
  * page are not read, and what the slots behind its last token hold (NaN
  * included) has no influence; values of stored tokens are finite (those that
- * the causal order hides from a row are multiplied by 0, as in fa_fwd).
+ * the causal order hides from a row are multiplied by 0, as in fa_fwd).  A
+ * row of the two attention calls with a score of NaN or +infinity has O = lse =
+ * NaN, however the work is split (a score of -infinity counts as hidden); no
+ * other row is touched by it.
  */
 
 /*

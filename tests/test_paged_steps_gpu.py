@@ -1,8 +1,8 @@
 """Steps of a server whose prefix has a pass of its own: append, prefix pass,
 own keys and (where these are split) the join run one behind the other on
-inputs that change from step to step, eager and captured; a step's kernels on a
-shared workspace and on two streams.  Each test first makes sure that its sizes
-take that path: then, and only then, decode needs a workspace."""
+inputs that change from step to step, eager and captured; rows that are no
+numbers on each path.  A test first makes sure that its sizes take the path it is
+for: results are joined through the workspace then, and only then is one needed."""
 
 import pytest
 import torch
@@ -141,3 +141,45 @@ def test_layers_in_a_row_equal_calls_apart(wide):
     for got in (in_a_row, in_a_graph):
         for (a, la), (b, lb) in zip(got, want):
             assert all(torch.equal(x, y) for x, y in zip(a, b)) and torch.equal(la, lb)
+
+
+NOT_NUMBERS = [
+    # Hq, Hkv, N, d, P, prefix, lens, table slack, whether decode / the forward
+    # pass join partial results, what is special
+    (8, 2, 2, 128, 16, 32, (300, 40), 1, False, False, "decode in one kernel"),
+    (8, 2, 3, 128, 64, 1024, (1100, 1030, 1500), 1, True, True, "prefix pass"),
+    (4, 4, 1, 64, 32, 640, (5000, 700), 40, True, True, "own keys split"),
+    (8, 2, 130, 64, 16, 0, (400, 190), 1, None, False, "forward, pairs"),
+    (8, 2, 20, 128, 16, 0, (2000, 1500), 1, None, True, "forward, keys split"),
+]
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")], ids=["nan", "inf"])
+@pytest.mark.parametrize("case", NOT_NUMBERS, ids=lambda c: c[-1].replace(" ", "_"))
+def test_a_query_that_is_no_number_shows(case, bad):
+    """softmax over scores with a NaN or +inf among them is NaN: so are O and
+    lse of that row (a score of inf in every key of one sign, which would leave
+    only -inf, does not happen with this many keys); the other rows of its
+    tile, warp and sequence stay right."""
+    Hq, Hkv, N, d, P, prefix, lens, slack, joins, forward_joins, _ = case
+    B = len(lens)
+    kc, vc, table, tl = pr.make_cache(7, Hkv, d, P, lens, BF, prefix=prefix, table_slack=slack)
+    q = torch.randn((B, Hq, N, d), generator=torch.Generator().manual_seed(5)).to(BF)
+    ref = pr.attention(q, kc, vc, table, lens, [N] * B, pr.default_scale(d))
+    hit = torch.zeros((B, Hq, N), dtype=torch.bool)
+    hit[0, 1, N - 1] = hit[B - 1, Hq - 1, 0] = True
+    q[hit, 3] = bad
+    dev = [t.to(DEV) for t in (q, kc, vc, table, tl)]
+    sizes = (B, Hq, Hkv, N, d, P, table.shape[1])
+    assert (binding.fa_fwd_paged_workspace_bytes(*sizes) > 0) == forward_joins
+    calls = [binding.attention_fwd_paged(*dev)]
+    if joins is not None:
+        assert (binding.fa_decode_prefix_workspace_bytes(*sizes, prefix) > 0) == joins
+        calls.append(binding.attention_decode_prefix(*dev, prefix))
+    tp.ok()
+    for o, lse in calls:
+        o, lse = o.cpu(), lse.cpu()
+        assert bool(torch.isnan(o[hit]).all()) and bool(torch.isnan(lse[hit]).all())
+        o[hit] = torch.from_numpy(ref[0])[hit].to(BF)
+        lse[hit] = torch.from_numpy(ref[1])[hit].float()
+        pr.check_attention(o, lse, ref, BF, [N] * B)
