@@ -641,12 +641,12 @@ def _allocating(device, stream):
 def cache_append(q, k, v, k_cache, v_cache, block_table, seq_lens, inv_freq=None, new_lens=None,
                  interleaved: bool = False, stream=None):
     """Allocates the rotated queries and runs fa_append_paged; returns them
-    (None when q is None).  Rows behind a sequence's new tokens are zero."""
+    (None when q is None).  Rows behind a sequence's new tokens, and those of
+    idle (length 0) and refused sequences, are zero."""
     q_out = None
     if q is not None:
         with _allocating(k.device, stream):
-            make = torch.empty if new_lens is None else torch.zeros
-            q_out = make(q.shape, device=q.device, dtype=q.dtype)
+            q_out = torch.zeros(q.shape, device=q.device, dtype=q.dtype)
     fa_append_paged(q, k, v, q_out, None, k_cache, v_cache, block_table, seq_lens, new_lens, inv_freq, interleaved, stream)
     return q_out
 

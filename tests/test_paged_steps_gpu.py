@@ -183,3 +183,26 @@ def test_a_query_that_is_no_number_shows(case, bad):
         o[hit] = torch.from_numpy(ref[0])[hit].to(BF)
         lse[hit] = torch.from_numpy(ref[1])[hit].float()
         pr.check_attention(o, lse, ref, BF, [N] * B)
+
+
+@pytest.mark.parametrize("new", [None, (1, 1, 1, 1, 1)], ids=["all_new", "new_lens"])
+def test_queries_of_idle_and_refused_sequences_come_back_as_zeros(new):
+    """cache_append's rows that no token of the call fills, in memory that held
+    NaN before: sequence 1 is idle, sequence 3 longer than its table."""
+    B, Hq, Hkv, d, P = 5, 8, 2, 128, 16
+    g = torch.Generator().manual_seed(4)
+    q, k, v = (torch.randn((B, h, 1, d), generator=g).to(BF).to(DEV) for h in (Hq, Hkv, Hkv))
+    caches = [torch.zeros((2 * B, Hkv, P, d), dtype=BF, device=DEV) for _ in range(2)]
+    table = torch.arange(2 * B, dtype=torch.int32, device=DEV).view(B, 2)
+    lens = torch.tensor([3, 0, 20, 2 * P + 1, 32], dtype=torch.int32, device=DEV)
+    nl = None if new is None else torch.tensor(new, dtype=torch.int32, device=DEV)
+    freq = pr.inv_freq(d).to(DEV)
+    for _ in range(3):
+        held = [torch.full((B, Hq, 1, d), float("nan"), dtype=BF, device=DEV) for _ in range(64)]
+        del held
+        out = binding.cache_append(q, k, v, *caches, table, lens, freq, nl)
+        assert binding.fa_get_device_status() == binding.FA_ERR_INVALID_ARG
+        assert bool((out[1] == 0).all()) and bool((out[3] == 0).all())
+        for b in (0, 2, 4):
+            want, mag = pr.rotated(q[b].cpu(), lens[b:b + 1].cpu() - 1, pr.inv_freq(d), False)
+            pr.check_rotated(out[b].cpu(), want, mag, f"q of sequence {b}")
