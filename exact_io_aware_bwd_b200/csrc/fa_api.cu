@@ -23,6 +23,19 @@
 #include "fa_paged.cuh"
 #include "fa_prefix.cuh"
 
+// The kernel ids in the status word say which kernel recorded an error.
+namespace fa {
+constexpr uint32_t kKernelIds[] = {kKernFwd, kKernBwdPre, kKernBwd, kKernBwdPost, kKernSelftest, kKernDecode,
+                                   kKernDecodeMerge, kKernFwdFp8, kKernPaged, kKernPrefixOwn, kKernAppend};
+constexpr bool ids_differ() {
+  for (const uint32_t& a : kKernelIds)
+    for (const uint32_t& b : kKernelIds)
+      if (&a != &b && a == b) return false;
+  return true;
+}
+static_assert(ids_differ(), "two kernels share an id");
+}  // namespace fa
+
 namespace {
 
 using fa::FwdLayout;

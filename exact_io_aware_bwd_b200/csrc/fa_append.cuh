@@ -33,7 +33,7 @@
 
 namespace fa {
 
-constexpr uint32_t kKernAppend = 12;
+constexpr uint32_t kKernAppend = 15;
 constexpr int kAppendThreads = 256;
 // Heads whose loads a thread has in flight (2, or 3 at four resident blocks:
 // 83-85 us on the prompt above against 80).

@@ -53,3 +53,12 @@ def test_tables_and_lengths_are_not_read_as_constants(file, kernel):
     """__ldg (ld.global.nc) asks that nobody writes the data while the kernel
     is resident; a dependent launch is resident before its inputs are written."""
     assert "__ldg" not in body(source(file), kernel)
+
+
+def test_kernel_ids_differ():
+    """The id in the status word says which kernel recorded an error."""
+    ids = {}
+    for name in sorted(os.listdir(CSRC)):
+        for kernel, value in re.findall(r"constexpr uint32_t (kKern[A-Z]\w*) = (\d+);", source(name)):
+            ids.setdefault(int(value), []).append(kernel)
+    assert len(ids) >= 11 and all(len(k) == 1 for k in ids.values()), ids

@@ -206,3 +206,19 @@ def test_queries_of_idle_and_refused_sequences_come_back_as_zeros(new):
         for b in (0, 2, 4):
             want, mag = pr.rotated(q[b].cpu(), lens[b:b + 1].cpu() - 1, pr.inv_freq(d), False)
             pr.check_rotated(out[b].cpu(), want, mag, f"q of sequence {b}")
+
+
+APPEND_ID, PAGED_ID, OWN_ID = 15, 13, 14     # bits 8-15 of the status word: the kernel that met the error
+
+
+def test_the_status_word_names_the_kernel():
+    kc, vc, table, tl = pr.make_cache(3, 2, 64, 16, [40, 30], BF)
+    tl[1] = table.shape[1] * 16 + 1
+    dev = [t.to(DEV) for t in (kc, vc, table, tl)]
+    q = torch.ones((2, 4, 3, 64), dtype=BF, device=DEV)
+    for call, kernel in ((lambda: binding.attention_fwd_paged(q, *dev), PAGED_ID),
+                         (lambda: binding.attention_decode_prefix(q, *dev, 16), OWN_ID)):
+        call()
+        assert binding.fa_peek_device_status_word() >> 8 & 255 == kernel
+        assert binding.fa_get_device_status() == binding.FA_ERR_INVALID_ARG
+    tp.ok()
