@@ -211,6 +211,50 @@ def test_queries_of_idle_and_refused_sequences_come_back_as_zeros(new):
 APPEND_ID, PAGED_ID, OWN_ID = 15, 13, 14     # bits 8-15 of the status word: the kernel that met the error
 
 
+@pytest.mark.parametrize("with_out", [False, True], ids=["cache_only", "q_out_k_out"])
+@pytest.mark.parametrize("bad", ["page", "page_negative", "too_long", "new_too_many", "new_negative", "short"])
+def test_a_refused_append_leaves_every_other_slot_alone(bad, with_out):
+    """Both whole caches bit for bit: the good sequence's tokens, those of the
+    bad one that sit on good pages (none when its lengths do not fit), nothing
+    else; rows of q_out and k_out of a refused sequence as they were."""
+    Hq, Hkv, N, d, P = 4, 2, 20, 64, 16
+    kc, vc, table, tl = pr.make_cache(3, Hkv, d, P, [40, 30], BF)
+    new = torch.tensor([20, 20], dtype=torch.int32)
+    good_table = table.clone()
+    if bad == "page":
+        table[1, 1] = kc.shape[0]
+    elif bad == "page_negative":
+        table[1, 1] = -7
+    elif bad == "too_long":
+        tl[1] = table.shape[1] * P + 1
+    elif bad == "new_too_many":
+        new[1] = N + 1
+    elif bad == "new_negative":
+        new[1] = -1
+    else:
+        tl[1] = 19
+    g = torch.Generator().manual_seed(4)
+    q, k, v = (torch.randn((2, h, N, d), generator=g).to(BF) for h in (Hq, Hkv, Hkv))
+    want_k, want_v = kc.clone(), vc.clone()
+    by_page = bad.startswith("page")
+    for b, pos in ((0, torch.arange(20, 40)), (1, torch.arange(10, 16 if by_page else 10))):
+        t = pos - int(pos[0]) if len(pos) else pos
+        page = good_table[b].long()[pos // P]
+        want_k[page, :, pos % P], want_v[page, :, pos % P] = k[b, :, t].transpose(0, 1), v[b, :, t].transpose(0, 1)
+    kd, vd = kc.to(DEV), vc.to(DEV)
+    q_out, k_out = (torch.full((2, h, N, d), 7.0, dtype=BF, device=DEV) if with_out else None for h in (Hq, Hkv))
+    binding.fa_append_paged(q.to(DEV) if with_out else None, k.to(DEV), v.to(DEV), q_out, k_out, kd, vd, table.to(DEV),
+                            tl.to(DEV), new.to(DEV), None)
+    assert binding.fa_peek_device_status_word() >> 8 & 255 == APPEND_ID
+    assert binding.fa_get_device_status() == binding.FA_ERR_INVALID_ARG
+    bits = lambda t: t.cpu().view(torch.int16)
+    assert torch.equal(bits(kd), bits(want_k)) and torch.equal(bits(vd), bits(want_v))
+    if with_out:
+        for got, src in ((q_out, q), (k_out, k)):
+            assert torch.equal(got[0].cpu(), src[0])
+            assert torch.equal(got[1].cpu(), src[1]) if by_page else bool((got[1] == 7).all())
+
+
 def test_the_status_word_names_the_kernel():
     kc, vc, table, tl = pr.make_cache(3, 2, 64, 16, [40, 30], BF)
     tl[1] = table.shape[1] * 16 + 1
