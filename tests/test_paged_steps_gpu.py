@@ -266,3 +266,82 @@ def test_the_status_word_names_the_kernel():
         assert binding.fa_peek_device_status_word() >> 8 & 255 == kernel
         assert binding.fa_get_device_status() == binding.FA_ERR_INVALID_ARG
     tp.ok()
+
+
+def joining_calls(seed, dtype):
+    """Calls that all join partial results through a workspace, each with its
+    reference: decode behind a prefix pass, the same with its own keys split,
+    the forward pass with its keys split.  (name, inputs, prefix, reference,
+    new tokens, bytes needed)"""
+    Hq, Hkv, d, P = 8, 2, 128, 16
+    calls = []
+    for i, (prefix, lens, N, slack) in enumerate(((1024, (1100, 1030, 1500), 1, 1), (2048, (2100, 2050), 4, 300))):
+        kc, vc, table, tl = pr.make_cache(seed + i, Hkv, d, P, lens, dtype, prefix=prefix, table_slack=slack)
+        q = torch.randn((len(lens), Hq, N, d), generator=torch.Generator().manual_seed(seed + i)).to(dtype)
+        ref = pr.attention(q, kc, vc, table, lens, [N] * len(lens), pr.default_scale(d))
+        dev = [t.to(DEV) for t in (q, kc, vc, table, tl)]
+        sizes = (len(lens), Hq, Hkv, N, d, P, table.shape[1])
+        calls.append(("prefix", dev, prefix, ref, [N] * len(lens), binding.fa_decode_prefix_workspace_bytes(*sizes, prefix)))
+        calls.append(("paged", dev, prefix, ref, [N] * len(lens), binding.fa_fwd_paged_workspace_bytes(*sizes)))
+    assert all(c[5] > 0 for c in calls)
+    return calls
+
+
+def run_call(call, o, lse, ws, stream=None):
+    name, dev, prefix, _, _, _ = call
+    scale = pr.default_scale(dev[0].shape[3])
+    if name == "prefix":
+        binding.fa_decode_prefix(*dev, o, lse, scale, prefix, ws, stream)
+    else:
+        binding.fa_fwd_paged(*dev, None, o, lse, scale, ws, stream)
+
+
+def outputs(call):
+    q = call[1][0]
+    return torch.full_like(q, float("nan")), torch.full(q.shape[:3], float("nan"), device=DEV)
+
+
+def test_graphs_that_join_share_a_workspace():
+    """Four captured calls over one workspace, replayed in turn: neither leaves
+    anything the other depends on."""
+    calls = joining_calls(1, BF)
+    ws = workspace(max(c[5] for c in calls))
+    graphs = []
+    for c in calls:
+        o, lse = outputs(c)
+        run_call(c, o, lse, ws)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run_call(c, o, lse, ws)
+        graphs.append((graph, o, lse))
+    for order in ((0, 1, 2, 3), (3, 1, 0, 2), (2, 2, 0, 0, 1, 3, 1)):
+        for i in order:
+            graphs[i][1].fill_(float("nan")), graphs[i][2].fill_(float("nan"))
+        for i in order:
+            graphs[i][0].replay()
+        for i in set(order):
+            pr.check_attention(graphs[i][1], graphs[i][2], calls[i][3], BF, calls[i][4])
+    tp.ok()
+
+
+def test_joining_calls_on_two_streams_do_not_meet():
+    """Two streams, each with a workspace of its own that all its calls use in
+    turn, a row of calls in flight on both."""
+    sides = []
+    for seed in (10, 20):
+        calls = joining_calls(seed, FP)
+        sides.append((torch.cuda.Stream(), calls, workspace(max(c[5] for c in calls))))
+    torch.cuda.synchronize()
+    results = [[[outputs(c) for c in calls] for _ in range(5)] for _, calls, _ in sides]
+    torch.cuda.synchronize()
+    for turn in range(5):
+        for i in range(4):
+            for side, (stream, calls, ws) in enumerate(sides):
+                run_call(calls[i], *results[side][turn][i], ws, stream)
+    torch.cuda.synchronize()
+    for (_, calls, _), turns in zip(sides, results):
+        for turn in turns:
+            for c, (o, lse) in zip(calls, turn):
+                pr.check_attention(o, lse, c[3], FP, c[4])
+    tp.ok()
