@@ -301,7 +301,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_paged_kernel(const __grid_c
       auto entry = [&](int rel) { return pg0 + rel < n_pages ? row_table[pg0 + rel] : -1; };
       if (it.splits > 1) cur = entry(lane), nxt = entry(32 + lane);
       bool ok = true;
-      for (int kt = 0; kt < it.n_kv; ++kt) {
+      int kt = 0;  // key tiles issued
+      for (; kt < it.n_kv; ++kt) {
         const int rel = kt * ppt;
         if (kt > 0 && rel % 32 == 0) {
           cur = nxt;
@@ -335,15 +336,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fa_paged_kernel(const __grid_c
         }
         __syncwarp();
       }
-      // The copies in flight land before the block exits (at once, unless a
-      // wait ran out: the MMA warp waits for every tile).
-      if (ok) {
-        if (which == 0) mbar_wait_drain(q_full, 0, kKernPaged, 9, 2);
-        for (int k = max(0, it.n_kv - NS); k < it.n_kv; ++k) {
-          const int n = 2 * k + which;
-          if (n + NS >= 2 * it.n_kv)  // else the slot was filled again: it had landed
-            mbar_wait_drain(&slot_full[n % NS], (n / NS) & 1, kKernPaged, warp, 3);
-        }
+      // The copies in flight land before the block exits: at once, unless a
+      // wait ran out (the MMA warp waits for every tile).  Then each of the
+      // warp's last tiles is waited for, one whose slot the other warp filled
+      // again perhaps for nothing, up to the limit of a wait.
+      if (which == 0) mbar_wait_drain(q_full, 0, kKernPaged, 9, 2);
+      for (int k = max(0, kt - NS); k < kt; ++k) {
+        const int n = 2 * k + which;
+        if (!ok || n + NS >= 2 * it.n_kv)  // else the slot was filled again: it had landed
+          mbar_wait_drain(&slot_full[n % NS], (n / NS) & 1, kKernPaged, warp, 3);
       }
     }
   } else if (warp == 8) {

@@ -317,6 +317,9 @@ __global__ void __launch_bounds__(kOwnThreads, own_blocks_per_sm(HD)) fa_prefix_
     st += kStage, ++st_bar;
     if (st == ring_end) st = ring, st_bar = full, phase ^= 1;
   }
+  // nothing is in flight here, unless a wait above ran out
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncwarp();
 
   // The warp's rows into its ring.
   float* sO = reinterpret_cast<float*>(sm + warp * NS * kStage);
