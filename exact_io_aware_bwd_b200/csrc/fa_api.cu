@@ -807,9 +807,16 @@ struct PagedPlan {
 
 // Splits by a model of the time, in steps of one row tile on one key tile
 // (1 us, half of a pair's): a block costs its steps and 5 more for its start
-// and end; blocks run in waves of one per SM; joining costs 5 steps for the
-// launch and the partial results' way through L2 (a row of a split: 8 d + 16
-// bytes at 5 TB/s).  Up to a wave of splits, at least 2 key tiles each.
+// and end; blocks run in whole waves of one per SM (they are about equally
+// long); joining costs 5 steps for the launch and the partial results' way
+// through L2 (a row of a split: 8 d + 16 bytes at 5 TB/s).  Up to a wave of
+// splits, at least 2 key tiles each.
+// Against the best of up to 36 other plans (each timed; 1 to 15 row tiles of 1,
+// 8 and 12 kv heads on 2048 to 65 536 keys; 1 to 8 sequences of 32 to 800 new
+// tokens behind 250 to 16 000) the plan is 0.2 % slower on average behind a
+// prefix and 2 % in the forward pass, at worst 5 and 23 %.  With fractions of a
+// wave from 4 waves on, 1.3 and 3 %, at worst 29 (15 row tiles x 8 heads on
+// 65 536 keys: 704 us in 5 splits of singles, 548 in 7 of pairs) and 39 %.
 PagedPlan paged_plan(int B, int Hq, int Hkv, int N, int d, int64_t keys, bool prefix) {
   PagedPlan pl;
   const int G = Hq / Hkv;
@@ -828,22 +835,22 @@ PagedPlan paged_plan(int B, int Hq, int Hkv, int N, int d, int64_t keys, bool pr
   pl.n_pairs = 0;
   pl.S = pl.S_single = 1;
   double best = 1e300;
-  // Pairs read each key once for two row tiles.  While row tiles one by one do
-  // not fill the GPU either, those: an odd number of them always (3 tiles x 8
-  // heads on 65 536 keys: 161 us against 167 with a pair and an odd one), an
-  // even number where that is modelled a tenth faster (2 tiles x 32 on 16 000
-  // keys, modelled alike: 76.7 us against 74.8 in pairs).
+  // Pairs read each key once for two row tiles: 3 % in favour of pairs where
+  // the model puts both alike.  (8 heads on 65 536 keys, pairs against singles:
+  // 2 row tiles 84.0 and 83.0 us, 3: 118.8 and 114.1, 4: 141 and 156, 6: 205 and
+  // 213, 9: 306 and 331.)  Row tiles one by one only while they do not fill
+  // the GPU.
   for (const int64_t pairs : {static_cast<int64_t>(pl.n_tiles / 2), static_cast<int64_t>(0)}) {
     const int64_t odd = pl.n_tiles - 2 * pairs;
     for (int64_t S = 1; S <= cap; ++S) {
       const int64_t Ss = odd ? (pairs ? (S + 1) / 2 : S) : 1;
       const int64_t blocks = pl.owners * (pairs * S + odd * Ss);
       if (S > 1 && blocks > 8 * fa::kDecodeSMs) break;  // the GPU is full
-      const double waves = static_cast<double>(blocks) / fa::kDecodeSMs;
+      const double waves = static_cast<double>((blocks + fa::kDecodeSMs - 1) / fa::kDecodeSMs);
       const double steps = std::max(pairs ? 2.0 * ((tiles + S - 1) / S) : 0.0, odd ? 1.0 * ((tiles + Ss - 1) / Ss) : 0.0);
-      double cost = (waves <= 4 ? std::ceil(waves) : waves) * (steps + 5);
+      double cost = waves * (steps + 5);
       if (S > 1 || prefix) cost += 5 + static_cast<double>(pl.rows()) * S * (8.0 * d + 16) / 5e12 / 1e-6;
-      if (!pairs) cost *= pl.n_tiles % 2 ? 0.99 : 1.1;
+      if (!pairs) cost *= 1.03;
       if (cost < best) {
         best = cost;
         pl.n_pairs = static_cast<int>(pairs);

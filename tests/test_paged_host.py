@@ -1,13 +1,15 @@
 """What can be seen of the paged-cache kernels without a GPU: that each kernel
 launched as a programmatic dependent (scheduled while the kernel before it still
-runs) waits for that kernel before it touches global memory."""
+runs) waits for that kernel before it touches global memory, and how a pass is
+cut into blocks."""
 
 import os
 import re
 
 import pytest
 
-from exact_io_aware_bwd_b200.build import CSRC
+from exact_io_aware_bwd_b200 import binding
+from exact_io_aware_bwd_b200.build import CSRC, build
 
 KERNELS = [("fa_append.cuh", "fa_append_kernel"), ("fa_paged.cuh", "fa_paged_kernel"),
            ("fa_paged.cuh", "fa_paged_merge_kernel"), ("fa_prefix.cuh", "fa_prefix_own_kernel")]
@@ -62,3 +64,38 @@ def test_kernel_ids_differ():
         for kernel, value in re.findall(r"constexpr uint32_t (kKern[A-Z]\w*) = (\d+);", source(name)):
             ids.setdefault(int(value), []).append(kernel)
     assert len(ids) >= 11 and all(len(k) == 1 for k in ids.values()), ids
+
+
+# ------------------------------------------------------ how a pass is cut
+
+SMS = 148
+
+
+def steps(form, n_tiles, owners, key_tiles, S, d):
+    """Time of a pass (in us) in whole waves of blocks: a block takes a step
+    for each of its row tiles and key tiles and 5 more, in pairs of row tiles
+    (an odd one alone, in half the splits) or one by one.  Joining moves
+    8 d + 16 bytes of each row and split at 5 TB/s."""
+    pairs = n_tiles // 2 if form == "pairs" else 0
+    odd = n_tiles - 2 * pairs
+    if form == "pairs" and not pairs:
+        return float("inf")
+    S_odd = (S + 1) // 2 if pairs else S
+    blocks = owners * (pairs * S + odd * S_odd)
+    of_a_block = max(2 * -(-key_tiles // S) if pairs else 0, -(-key_tiles // S_odd) if odd else 0)
+    return -(-blocks // SMS) * (of_a_block + 5) + owners * n_tiles * 128 * S * (8 * d + 16) / 5e6
+
+
+@pytest.mark.parametrize("n_tiles", [1, 2, 3, 4, 5, 6, 7, 9, 11, 13, 15, 17, 18])
+@pytest.mark.parametrize("keys", [8192, 65536])
+def test_a_prefix_pass_is_not_cut_into_mostly_empty_waves(n_tiles, keys):
+    """The number of splits, read off the workspace, allows a time within a
+    tenth of the best one."""
+    Hq, Hkv, d, P, seqs = 32, 8, 128, 64, 32
+    build()
+    nbytes = binding.fa_decode_prefix_workspace_bytes(seqs * n_tiles, Hq, Hkv, 1, d, P, keys // P + 1, keys)
+    splits = nbytes // (Hkv * n_tiles * 128 * (4 * d + 8))
+    assert splits * Hkv * n_tiles * 128 * (4 * d + 8) == nbytes
+    of = lambda form, S: steps(form, n_tiles, Hkv, keys // 128, S, d)
+    best = min(of(form, S) for form in ("pairs", "singles") for S in range(1, 65))
+    assert min(of("pairs", splits), of("singles", splits)) <= 1.1 * best
