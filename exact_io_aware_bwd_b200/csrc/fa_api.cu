@@ -888,11 +888,17 @@ int own_splits(int B, int Hkv, int64_t own_keys) {
 
 // Keys of the prefix that get a pass of their own.  A short one is read with
 // the own keys of every sequence instead: one kernel, and while the blocks'
-// reads of it stay few (32/8 heads of 128, prefixes of 128 to 512 keys: 8.5-10.5
-// us with the pass, 5.6-9.7 without, for up to 16 sequences; 1024 keys: 11
-// against 14; 32 sequences: 11.5 against 11.7 at 512 keys).
-int own_pass_prefix(int B, int Hkv, int prefix_len) {
-  return prefix_len <= 512 && static_cast<int64_t>(B) * Hkv * prefix_len <= 65536 ? 0 : prefix_len;
+// reads of it stay few.  Both ways timed (own keys' kernel alone | pass and own
+// keys) at 396 sizes: 32/8, 12/12, 16/16, 8/1 and 28/4 heads of 64 and 128, 1 to
+// 32 rows, 1 to 128 sequences, 64 to 1024 keys.  32/8 x 128: 512 keys, 1 to 32
+// sequences 9.8-12.7 | 12.5-15.2 us, 64: 24.2 | 21.0; 256 keys, 64: 17.6 | 20.0,
+// 128: 28.1 | 27.1; 768 keys, 4: 12.8 | 13.8; 1024 keys, 4: 15.3 | 14.3.  Heads
+// of 64 are read in half the time (256 keys, 128 sequences: 17.0 | 18.9).  The
+// rule is 0.4 % above the better of the two on average; at most 8 % where it
+// leaves the pass out (4 tokens of 1 sequence, 8/1 heads, 768 keys: 25.6 | 23.7)
+// and 19 % where it does not (4 tokens of 16, 32/8, 1024: 19.1 | 22.7).
+int own_pass_prefix(int B, int Hkv, int d, int prefix_len) {
+  return prefix_len <= 768 && static_cast<int64_t>(B) * Hkv * prefix_len * d <= (1 << 24) ? 0 : prefix_len;
 }
 
 size_t own_bytes(int B, int Hq, int N, int d, int S) {
@@ -1132,7 +1138,7 @@ size_t fa_decode_prefix_workspace_bytes(int B, int Hq, int Hkv, int Nq, int d, i
   if (B <= 0 || Hq <= 0 || Hkv <= 0 || Nq <= 0 || d <= 0 || page_size <= 0 || max_pages <= 0 || prefix_len < 0 ||
       Hq % Hkv != 0 || static_cast<int64_t>(Hq / Hkv) * Nq > fa::kDecodeMaxRows)
     return 0;
-  const int pass = own_pass_prefix(B, Hkv, prefix_len);
+  const int pass = own_pass_prefix(B, Hkv, d, prefix_len);
   return paged_plan(B, Hq, Hkv, Nq, d, pass, true).bytes(d) +
          own_bytes(B, Hq, Nq, d, own_splits(B, Hkv, static_cast<int64_t>(max_pages) * page_size - pass));
 }
@@ -1148,7 +1154,7 @@ fa_status_t fa_decode_prefix(const void* q, const void* k_cache, const void* v_c
   if (static_cast<int64_t>(Hq / Hkv) * Nq > fa::kDecodeMaxRows) return FA_ERR_UNSUPPORTED;
   if (B == 0) return FA_OK;
   if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !o || !lse) return FA_ERR_INVALID_ARG;
-  const int pass = own_pass_prefix(B, Hkv, prefix_len);
+  const int pass = own_pass_prefix(B, Hkv, d, prefix_len);
   const PagedPlan pl = paged_plan(B, Hq, Hkv, Nq, d, pass, true);
   const size_t need = pl.bytes(d) + own_bytes(B, Hq, Nq, d,
                                               own_splits(B, Hkv, static_cast<int64_t>(max_pages) * page_size - pass));

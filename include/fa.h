@@ -335,7 +335,7 @@ fa_status_t fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache
  * entries of the other sequences' tables for it are not read.  A sequence
  * shorter than the prefix sees the part up to its own length.  Limits as
  * fa_decode_paged ((Hq / Hkv) * Nq <= 32).  The prefix's slots all hold
- * tokens.  A prefix of up to 512 tokens may be read by each sequence instead,
+ * tokens.  A prefix of up to 768 tokens may be read by each sequence instead,
  * where that is faster.  One to three kernels, launched as programmatic
  * dependents (see fa_decode_paged).
  * workspace (device, 16-byte aligned):

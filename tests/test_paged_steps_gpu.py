@@ -148,7 +148,7 @@ NOT_NUMBERS = [
     # pass join partial results, what is special
     (8, 2, 2, 128, 16, 32, (300, 40), 1, False, False, "decode in one kernel"),
     (8, 2, 3, 128, 64, 1024, (1100, 1030, 1500), 1, True, True, "prefix pass"),
-    (4, 4, 1, 64, 32, 640, (5000, 700), 40, True, True, "own keys split"),
+    (4, 4, 1, 64, 32, 1280, (5000, 1400), 40, True, True, "own keys split"),
     (8, 2, 130, 64, 16, 0, (400, 190), 1, None, False, "forward, pairs"),
     (8, 2, 20, 128, 16, 0, (2000, 1500), 1, None, True, "forward, keys split"),
 ]
@@ -345,3 +345,23 @@ def test_joining_calls_on_two_streams_do_not_meet():
             for c, (o, lse) in zip(calls, turn):
                 pr.check_attention(o, lse, c[3], FP, c[4])
     tp.ok()
+
+
+@pytest.mark.parametrize("prefix", [512, 768, 784, 1024])
+@pytest.mark.parametrize("B,d", [(2, 128), (40, 128), (40, 64), (90, 64), (130, 128)])
+def test_prefixes_with_and_without_a_pass_of_their_own(prefix, B, d):
+    """Up to 768 keys, and up to 2^24 values of a head's keys in all that the
+    blocks read, are taken with the own keys; idle sequences, ones shorter than
+    the prefix or ending with it among the others."""
+    Hq, Hkv, Nq, P = 4, 2, 2, 16
+    lens = tuple((prefix + 2 + 7 * i, 0, prefix - 3 * i - 1, prefix, prefix + 1, 2)[i % 6 if i else 0] for i in range(B))
+    kc, vc, table, tl = pr.make_cache(B, Hkv, d, P, lens, BF, prefix=prefix)
+    alone = prefix <= 768 and B * Hkv * prefix * d <= 1 << 24
+    assert (binding.fa_decode_prefix_workspace_bytes(B, Hq, Hkv, Nq, d, P, table.shape[1], prefix) == 0) == alone
+    q = torch.randn((B, Hq, Nq, d), generator=torch.Generator().manual_seed(B)).to(BF)
+    ref = pr.attention(q, kc, vc, table, lens, [Nq] * B, pr.default_scale(d))
+    seen = table.clone()
+    seen[1:, :prefix // P] = -1
+    o, lse = binding.attention_decode_prefix(q.to(DEV), kc.to(DEV), vc.to(DEV), seen.to(DEV), tl.to(DEV), prefix)
+    tp.ok()
+    pr.check_attention(o, lse, ref, BF, [Nq] * B)
