@@ -877,13 +877,17 @@ struct PagedArgs {
   fa_dtype_t dtype;
 };
 
-// Splits of each sequence's own keys: one while there are two blocks per SM,
-// else enough for that, of at least 1024 keys each (joining them takes another
-// kernel, about the time of 1024 keys).
+// Splits of each sequence's own keys: as many as bring the blocks nearest to
+// two per SM, of at least 1024 keys each.  8192 own keys, 32/8 heads of 128: 1
+// sequence 83 us in one piece, 18.9 in 8; 8 sequences 84 and 49 in 4; but 28 and
+// 32 sequences 142 and 162 us in one piece, 163 and 188 in two (with 2048 keys
+// 40 and 46, 51 and 58).  The 1024: own_keys is what the table has room for.
+// Full tables would gain from shorter splits (2048 keys of 1 sequence: 16.9 us
+// in 2, 10.9 in 8), but sequences that fill little of theirs pay for each (150
+// keys: 5.1 us in one piece, 7.2 in 2, 10.8 in 16).
 int own_splits(int B, int Hkv, int64_t own_keys) {
   const int64_t items = static_cast<int64_t>(B) * Hkv, slots = 2 * fa::kDecodeSMs;
-  if (items >= slots) return 1;
-  return static_cast<int>(std::max<int64_t>(1, std::min((slots + items - 1) / items, own_keys / 1024)));
+  return static_cast<int>(std::max<int64_t>(1, std::min((2 * slots + items) / (2 * items), own_keys / 1024)));
 }
 
 // Keys of the prefix that get a pass of their own.  A short one is read with

@@ -365,3 +365,22 @@ def test_prefixes_with_and_without_a_pass_of_their_own(prefix, B, d):
     o, lse = binding.attention_decode_prefix(q.to(DEV), kc.to(DEV), vc.to(DEV), seen.to(DEV), tl.to(DEV), prefix)
     tp.ok()
     pr.check_attention(o, lse, ref, BF, [Nq] * B)
+
+
+@pytest.mark.parametrize("items", [1, 2, 3, 16, 36, 37])
+def test_own_keys_split_and_not(items):
+    """The number of splits is read off the workspace: two blocks per SM, or
+    the nearest number to it, and no split of fewer than 1024 keys."""
+    Hq, Hkv, Nq, d, P, room = 16, 8, 1, 128, 128, 8192
+    B = items
+    splits = max(1, min((2 * 296 + B * Hkv) // (2 * B * Hkv), room // 1024))
+    nbytes = binding.fa_decode_prefix_workspace_bytes(B, Hq, Hkv, Nq, d, P, room // P, 0)
+    assert nbytes == (B * Hq * Nq * splits * (d + 2) * 4 if splits > 1 else 0)
+    lens = tuple((1500, 1, 900, 0, 2100)[b % 5] for b in range(B))
+    kc, vc, table, tl = pr.make_cache(items, Hkv, d, P, lens, FP, table_slack=room // P - 17)
+    table = torch.cat([table, torch.full((B, room // P - table.shape[1]), -1, dtype=torch.int32)], 1)
+    q = torch.randn((B, Hq, Nq, d), generator=torch.Generator().manual_seed(B)).to(FP)
+    ref = pr.attention(q, kc, vc, table, lens, [Nq] * B, pr.default_scale(d))
+    o, lse = binding.attention_decode_prefix(*[t.to(DEV) for t in (q, kc, vc, table, tl)], 0)
+    tp.ok()
+    pr.check_attention(o, lse, ref, FP, [Nq] * B)
