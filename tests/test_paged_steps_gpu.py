@@ -384,3 +384,95 @@ def test_own_keys_split_and_not(items):
     o, lse = binding.attention_decode_prefix(*[t.to(DEV) for t in (q, kc, vc, table, tl)], 0)
     tp.ok()
     pr.check_attention(o, lse, ref, FP, [Nq] * B)
+
+
+def test_a_graph_of_copies_fills_a_fork_and_the_allocating_calls():
+    """The calls that allocate, captured between what a program captures with
+    them: copies of the step's inputs, a fill, a second stream that runs a
+    prompt's pass beside decode and joins it.  Replayed on other inputs it
+    gives bit for bit what the calls give one by one."""
+    B, Hq, Hkv, d, P, prefix = 6, 8, 2, 128, 32, 1024
+    lens = [prefix + 3 + 11 * b for b in range(B)]
+    kc, vc, table, _ = pr.make_cache(4, Hkv, d, P, [n + 30 for n in lens], BF, prefix=prefix)
+    g = torch.Generator().manual_seed(9)
+    table, freq = table.to(DEV), pr.inv_freq(d).to(DEV)
+    caches = [torch.nan_to_num(t).to(DEV) for t in (kc, vc)]
+    N = 20
+    sets = [[torch.randn((B, h, n, d), generator=g).to(BF).to(DEV) for h, n in ((Hq, 1), (Hkv, 1), (Hkv, 1), (Hq, N))]
+            + [torch.tensor([n + 1 + i for n in lens], dtype=torch.int32, device=DEV)] for i in range(4)]
+    here = [t.clone() for t in sets[0]]
+    filled = torch.zeros((4, 2), device=DEV)
+    side = torch.cuda.Stream()
+
+    def work(given, kc, vc, apart):
+        wait = torch.cuda.synchronize if apart else (lambda: None)
+        for dst, src in zip(here, given):
+            dst.copy_(src)
+        q, k, v, prompt, n = here
+        filled.zero_()
+        wait()
+        q_rot = binding.cache_append(q, k, v, kc, vc, table, n, freq)
+        wait()
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            second = binding.attention_fwd_paged(prompt, kc, vc, table, n)
+        wait()
+        first = binding.attention_decode_prefix(q_rot, kc, vc, table, n, prefix)
+        main.wait_stream(side)
+        wait()
+        return q_rot, *first, *second
+
+    want = []
+    own = [c.clone() for c in caches]
+    for given in sets:
+        want.append([t.clone() for t in work(given, *own, True)])
+    torch.cuda.synchronize()
+    own2 = [c.clone() for c in caches]
+    from_here = [t.clone() for t in sets[0]]
+    work(from_here, *[c.clone() for c in caches], False)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = work(from_here, *own2, False)
+    for given, expected in zip(sets, want):
+        for dst, src in zip(from_here, given):
+            dst.copy_(src)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, expected))
+    assert all(torch.equal(a, b) for a, b in zip(own, own2))
+    tp.ok()
+
+
+def test_two_threads_call_at_once():
+    """Each with its own stream, workspace and inputs."""
+    import threading
+    torch.cuda.synchronize()
+    failures = []
+
+    def run(seed):
+        try:
+            calls = joining_calls(seed, BF)
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                ws = workspace(max(c[5] for c in calls))
+                results = [[outputs(c) for c in calls] for _ in range(8)]
+                stream.synchronize()
+                for turn in results:
+                    for c, (o, lse) in zip(calls, turn):
+                        run_call(c, o, lse, ws, stream)
+                stream.synchronize()
+            for turn in results:
+                for c, (o, lse) in zip(calls, turn):
+                    pr.check_attention(o, lse, c[3], BF, c[4])
+        except BaseException as e:
+            failures.append(e)
+
+    threads = [threading.Thread(target=run, args=(s,)) for s in (30, 40)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failures, failures
+    tp.ok()
