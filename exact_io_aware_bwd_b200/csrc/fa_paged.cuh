@@ -11,7 +11,8 @@
 //             tile's rows end at nearly the same key and the group's heads
 //             share each key read;
 //   prefix    seqs = 128 / (G N) sequences times their G N rows: the whole
-//             batch reads each prefix key once per 256 rows.
+//             batch reads each prefix key once per row tile, or once per two
+//             where they are taken in pairs.
 // Either is one box of a 5-D tensor map over q (feature, head of the group,
 // token, kv head, sequence).
 //
@@ -41,12 +42,20 @@
 // of hidden keys are replaced, and the value rows of such slots are cleared
 // in shared memory before the product reads them (0 * NaN is not 0).
 //
+// The probabilities are rounded to the I/O type for the P V product: the tensor
+// core takes 16-bit operands (tf32 would halve its rate and double P's room in
+// tensor memory).  The sums l are of the unrounded values, O stays in 32 bits
+// until it is written.  Against 64 bits O is off by 2.3e-3 relative in bf16 and
+// 2.9e-4 in fp16; rounding O alone costs 1.7e-3 and 2.1e-4.
+//
 // What bounds it: with many row tiles the chain softmax -> P V -> next S of a
 // row tile, 1.1 + 0.9 us, two tiles in flight: 1.04 us a step at d = 128 (two
-// prompts of 4096 tokens behind 8192, 32 heads: 1060 us, 1160 TFLOP/s); with
-// one, memory and the block's start and end (16 384 shared keys of 8 heads, 67
-// MB, in 20 us).  The TMA engine takes about 40 ns a box: K and V tiles are
-// issued by a warp each, started before the block's other warps are set up.
+// prompts of 4096 tokens behind 6299 and 7983 cached ones, 32 heads: 1055-1075
+// us, 1150-1170 TFLOP/s, in short runs; 1240 us, 995 TFLOP/s, at the clock of a
+// long one); with one, memory and the block's start and end (16 384 shared keys
+// of 8 heads, 67 MB, in 19-22 us).  The TMA engine takes about 40 ns a box: K and
+// V tiles are issued by a warp each, started before the block's other warps are
+// set up.  168 registers a thread at launch, 36 bytes of spills.
 #pragma once
 
 #include <type_traits>

@@ -20,6 +20,9 @@
 // more than 8 (log2), the mask, the clearing of rows without a token and the
 // table look-up outside the common path.
 //
+// Probabilities are rounded to the I/O type for mma.sync, as in the row-tile
+// kernel, and bounded by 2^8; l, O and what is joined are in 32 bits.
+//
 // Each warp keeps its own running max and sum (with more than 16 rows, two
 // warps share the keys, one for each 16 rows).  The partial results of the
 // warps and of the prefix's splits meet at the end:

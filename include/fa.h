@@ -272,8 +272,8 @@ fa_status_t fa_decode_paged(const void* q, const void* k_cache, const void* v_ca
  * reported by fa_get_device_status as FA_ERR_INVALID_ARG; such a sequence
  * appends nothing (a bad entry: nothing on that page) and has O = 0, lse =
  * -inf (a bad entry: unspecified).  Table entries behind a sequence's last
- * page are not read, and what the slots behind its last token hold (NaN
- * included) has no influence; values of stored tokens are finite (those that
+ * page may be loaded but have no influence, whatever they hold, and nor has
+ * what the slots behind its last token hold (NaN included); values of stored tokens are finite (those that
  * the causal order hides from a row are multiplied by 0, as in fa_fwd).  A
  * row of the two attention calls with a score of NaN or +infinity has O = lse =
  * NaN, however the work is split (a score of -infinity counts as hidden); no
@@ -316,7 +316,9 @@ fa_status_t fa_append_paged(const void* q, const void* k, const void* v, const i
  * workspace (device, 16-byte aligned) of
  * fa_fwd_paged_workspace_bytes(B, Hq, Hkv, N, d, page_size, max_pages) bytes
  * holds partial results, when few rows meet a long table and the keys are
- * split over several blocks; NULL where that is 0.  One kernel, or two,
+ * split over several blocks; NULL where that is 0.  The split goes by the
+ * table's width, the lengths being on the device: a table many times wider than
+ * the sequences costs time (short prompts up to twice as much), never accuracy.  One kernel, or two,
  * launched as programmatic dependents (see fa_decode_paged).
  */
 size_t fa_fwd_paged_workspace_bytes(int B, int Hq, int Hkv, int N, int d, int page_size,
@@ -336,7 +338,8 @@ fa_status_t fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache
  * shorter than the prefix sees the part up to its own length.  Limits as
  * fa_decode_paged ((Hq / Hkv) * Nq <= 32).  The prefix's slots all hold
  * tokens.  A prefix of up to 768 tokens may be read by each sequence instead,
- * where that is faster.  One to three kernels, launched as programmatic
+ * where that is faster.  The own keys are split by the table's width, as in
+ * fa_fwd_paged.  One to three kernels, launched as programmatic
  * dependents (see fa_decode_paged).
  * workspace (device, 16-byte aligned):
  * fa_decode_prefix_workspace_bytes(B, Hq, Hkv, Nq, d, page_size, max_pages,
