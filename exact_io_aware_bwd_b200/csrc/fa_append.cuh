@@ -23,8 +23,9 @@
 // Bound by memory on prompts: 16 384 tokens of 32 / 8 heads of 128 (436 MB read
 // and written) in 72 us, 6.0 TB/s; by the launch on single tokens, 2.9 us.
 // Several heads' loads in flight a thread (78 us against 112 with one), three
-// resident blocks (80 registers, 24 to 32 bytes of spills) and 24 blocks per SM (72 us against 78 with
-// 4) got it there; ragged batches stay at the latency of their first loads.
+// resident blocks (80 registers, 24 to 32 bytes of spills) and 24 blocks per
+// SM (72 us against 78 with 4) got it there; ragged batches stay at the latency
+// of their first loads.
 #pragma once
 
 #include <type_traits>
